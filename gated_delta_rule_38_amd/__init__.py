@@ -10,13 +10,19 @@ raises if the library or a GPU is missing.
 Names follow the C ABI: ``prefill`` (kda_prefill / kda_prefill_ws),
 ``prefill_noalloc`` (kda_prefill_noalloc), ``workspace_size``, ``prep``
 (kda_prep), ``decode`` (kda_decode),
-``profile_enable``/``profile_read``.
+``profile_enable``/``profile_read``; and the operators around the recurrence
+(``include/kda_layer.h``, ``layer.py``): ``conv``, ``conv_decode``,
+``qk_norm``, ``rotary_frequencies``, ``ssm_prefill``, ``ssm_decode``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 from typing import Optional, Tuple
+
+from . import layer
+from .layer import (conv, conv_decode, qk_norm, rotary_frequencies, ssm_decode, ssm_prefill,  # noqa: F401
+                    ssm_workspace_size)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkda.so")
@@ -28,6 +34,9 @@ STATUS = {0: "KDA_OK", 1: "KDA_ERR_NULL", 2: "KDA_ERR_SHAPE", 3: "KDA_ERR_DTYPE"
 EXPORTS = ("kda_prefill", "kda_prefill_workspace_size", "kda_prefill_ws", "kda_prefill_noalloc", "kda_prep", "kda_decode",
            "kda_release_cached_workspace", "kda_profile_enable", "kda_profile_read", "kda_profile_read_kernels",
            "kda_status_string", "kda_last_error", "kda_abi_version",
+           # the operators around the recurrence (include/kda_layer.h)
+           "kda_conv", "kda_conv_decode", "kda_qk_norm", "kda_ssm_prefill", "kda_ssm_workspace_size",
+           "kda_ssm_prefill_ws", "kda_ssm_decode",
            # measurement probes (include/kda_peak.h)
            "kda_peak_stream", "kda_peak_mfma")
 
@@ -100,6 +109,7 @@ def load_library(path: str = LIB_PATH):
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []
     lib.kda_abi_version.restype = ctypes.c_int
+    layer.bind(lib)
     _lib = lib
     return lib
 

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_chunk.hip", "kda_chunk_pipe.hip", "kda_prep.hip", "kda_combine.hip", "kda_decode.hip",
-           "kda_peak.hip"]
+           "kda_peak.hip", "kda_layer_api.cpp", "kda_conv.hip", "kda_qk_norm.hip", "kda_ssm.hip", "kda_ssm_decode.hip"]
 # -packed-fp32-ops: no v_pk_*_f32 generation in device code.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -36,7 +36,7 @@ def build(verbose: bool = True) -> str:
     bdir = os.path.join(HERE, "_build")
     os.makedirs(bdir, exist_ok=True)
     objs = [os.path.join(bdir, os.path.splitext(s)[0] + ".o") for s in SOURCES]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
         list(ex.map(_compile, SOURCES, objs))
     tmp = LIB + ".tmp"
     r = subprocess.run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp],

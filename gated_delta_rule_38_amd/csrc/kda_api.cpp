@@ -26,12 +26,11 @@
 #include <string>
 #include <vector>
 
-#include "../../include/kda.h"
-#include "kda_launch.hpp"
+#include "kda_host.hpp"
 
-namespace {
+namespace kda_host {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 kda_status_t fail(kda_status_t st, const char *fmt, ...)
 {
@@ -48,10 +47,6 @@ kda_status_t hip_fail(hipError_t e, const char *what)
 {
     return fail(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
-
-struct Span {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi) in bytes; empty when lo == hi
-};
 
 size_t elem_size(int32_t dt) { return dt == KDA_BF16 ? 2 : 4; }
 
@@ -86,20 +81,6 @@ int64_t numel(const kda_tensor_t *t)
     return n;
 }
 
-// Strides of a token-major view as (batch, token, head) in elements.
-struct Tok {
-    int64_t sb = 0, st = 0, sh = 0;
-};
-
-struct Problem {
-    bool dense = true;
-    int64_t B = 0, T = 0, Ttot = 0, N = 0, H = 0, D = 0;
-    bool fp32 = false;
-    Tok q, k, v, g, beta, out;
-    int64_t s0_sn = 0, s0_sh = 0, s0_sr = 0, sT_sn = 0, sT_sh = 0, sT_sr = 0;
-    const kda_tensor_t *tq, *tk, *tv, *tg, *tb, *ts0, *tcu, *tout, *tsT;
-};
-
 kda_status_t check_basic(const kda_tensor_t *t, const char *name, bool allow_null)
 {
     if (!t) return allow_null ? KDA_OK : fail(KDA_ERR_NULL, "%s descriptor is NULL", name);
@@ -115,6 +96,175 @@ kda_status_t check_basic(const kda_tensor_t *t, const char *name, bool allow_nul
     if (!t->data && numel(t) > 0) return fail(KDA_ERR_NULL, "%s: data pointer is NULL", name);
     return KDA_OK;
 }
+
+// ------------------------------------------------------------------ environment
+// KDA_LOG=1: every plan to stderr.  KDA_CHECK=1: cu_seqlens checked on the device before
+// anything else is launched (one small kernel, a stream sync and a 4-byte read back).
+bool env_on(const char *name)
+{
+    const char *v = getenv(name);
+    return v && *v && strcmp(v, "0") != 0;
+}
+
+static std::mutex g_check_mu;                 // held for a whole check: one flag buffer per device
+static std::vector<int32_t *> g_check_flag;   // per device, allocated on first use
+
+kda_status_t run_device_checks(const DeviceChecks &c, hipStream_t st, int32_t *flags)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    // the lock covers the launches and the read-back, so that checks on other streams of the
+    // device never write the flags in between
+    std::lock_guard<std::mutex> lk(g_check_mu);
+    int32_t *flag = flags;
+    if (!flag) {
+        if ((int)g_check_flag.size() <= dev) g_check_flag.resize(dev + 1, nullptr);
+        if (!g_check_flag[dev] && (e = hipMalloc(&g_check_flag[dev], 256)) != hipSuccess) {
+            g_check_flag[dev] = nullptr;
+            return hip_fail(e, "device check buffer");
+        }
+        flag = g_check_flag[dev];
+    }
+    int32_t h[3] = {0, 0, 0};
+    if ((e = hipMemsetAsync(flag, 0, sizeof(h), st)) != hipSuccess) return hip_fail(e, "device check reset");
+    if (c.cu && (e = kda::launch_check_cu(c.cu, (int32_t)c.N, c.Ttot, flag, st)) != hipSuccess)
+        return hip_fail(e, "cu_seqlens check");
+    if (c.check_g && (e = kda::launch_check_g(c.g, flag + 1, st)) != hipSuccess) return hip_fail(e, "g range check");
+    if (c.slots && (e = kda::launch_check_slots(c.slots, (int32_t)c.R, (int32_t)c.P, flag + 2, st)) != hipSuccess)
+        return hip_fail(e, "slot check");
+    if ((e = hipMemcpyAsync(h, flag, sizeof(h), hipMemcpyDeviceToHost, st)) != hipSuccess ||
+        (e = hipStreamSynchronize(st)) != hipSuccess)
+        return hip_fail(e, "device check read-back");
+    if (h[0]) return fail(KDA_ERR_SHAPE, "cu_seqlens is not an offset array (cu[0] == 0, non-decreasing, cu[N] == %lld)",
+                          (long long)c.Ttot);
+    if (h[1]) {
+        if (c.g.lo == -INFINITY) return fail(KDA_ERR_RANGE, "g (logits) holds NaN");
+        return fail(KDA_ERR_RANGE, "g holds values outside [%g, %g] (or NaN)", (double)c.g.lo, (double)c.g.hi);
+    }
+    if (h[2]) return fail(KDA_ERR_ALIAS, "two requests name the same state slot with the state update on");
+    return KDA_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+int device_cus()
+{
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 256;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) return 256;
+    return cus;
+}
+
+// ------------------------------------------------------------- profiling
+struct ProfRec {
+    const char *name;
+    hipEvent_t a, b;
+};
+static std::mutex g_prof_mu;
+static std::vector<ProfRec> g_prof;                         // launches recorded since the last read
+static std::vector<std::pair<hipEvent_t, hipEvent_t>> g_prof_pool;   // idle event pairs
+static bool g_prof_on = false;
+
+// Event pairs come from a pool that profiling's enable call fills, so that a timed launch
+// costs two event records and no event creation.
+static hipError_t prof_pair(hipEvent_t &a, hipEvent_t &b)
+{
+    if (!g_prof_pool.empty()) {
+        a = g_prof_pool.back().first;
+        b = g_prof_pool.back().second;
+        g_prof_pool.pop_back();
+        return hipSuccess;
+    }
+    hipError_t e = hipEventCreate(&a);
+    if (e == hipSuccess) e = hipEventCreate(&b);
+    return e;
+}
+
+bool prof_on() { return g_prof_on; }
+
+hipError_t prof_begin(hipStream_t st, hipEvent_t &a, hipEvent_t &b)
+{
+    {
+        std::lock_guard<std::mutex> lk(g_prof_mu);
+        hipError_t e = prof_pair(a, b);
+        if (e != hipSuccess) return e;
+    }
+    return hipEventRecord(a, st);
+}
+
+hipError_t prof_end(const char *name, hipStream_t st, hipEvent_t a, hipEvent_t b)
+{
+    hipError_t e = hipEventRecord(b, st);
+    if (e != hipSuccess) return e;
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    g_prof.push_back(ProfRec{name, a, b});
+    return hipSuccess;
+}
+
+// The prefill entry points' workspace cache: one buffer per (device, stream), so calls on different
+// streams never share memory, and a buffer is only replaced after its own stream has
+// finished with it.  The lock is held until the call has enqueued its kernels: a call
+// from another thread on the same stream that grows the buffer then waits for them.
+static std::mutex g_ws_mu;
+struct CachedWs {
+    int dev = 0;
+    void *stream = nullptr;
+    void *p = nullptr;
+    size_t bytes = 0;
+};
+static std::vector<CachedWs> g_ws;
+
+kda_status_t with_cached_ws(size_t bytes, void *stream, kda_status_t (*run)(void *ws, void *arg), void *arg)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    CachedWs *cp = nullptr;
+    for (CachedWs &x : g_ws)
+        if (x.dev == dev && x.stream == stream) cp = &x;
+    if (!cp) {
+        g_ws.push_back(CachedWs{dev, stream, nullptr, 0});
+        cp = &g_ws.back();
+    }
+    CachedWs &c = *cp;
+    if (c.bytes < bytes) {
+        if (c.p) {
+            if ((e = hipStreamSynchronize((hipStream_t)stream)) != hipSuccess) return hip_fail(e, "workspace sync");
+            e = hipFree(c.p);
+            c.p = nullptr;
+            c.bytes = 0;
+            if (e != hipSuccess) return hip_fail(e, "workspace free");
+        }
+        if ((e = hipMalloc(&c.p, bytes)) != hipSuccess) {
+            c.p = nullptr;
+            return fail(KDA_ERR_WORKSPACE, "hipMalloc(%zu): %s", bytes, hipGetErrorString(e));
+        }
+        c.bytes = bytes;
+    }
+    return run(c.p, arg);
+}
+
+}  // namespace kda_host
+
+using namespace kda_host;
+
+namespace {
+
+// Strides of a token-major view as (batch, token, head) in elements.
+struct Tok {
+    int64_t sb = 0, st = 0, sh = 0;
+};
+
+struct Problem {
+    bool dense = true;
+    int64_t B = 0, T = 0, Ttot = 0, N = 0, H = 0, D = 0;
+    bool fp32 = false;
+    Tok q, k, v, g, beta, out;
+    int64_t s0_sn = 0, s0_sh = 0, s0_sr = 0, sT_sn = 0, sT_sh = 0, sT_sr = 0;
+    const kda_tensor_t *tq, *tk, *tv, *tg, *tb, *ts0, *tcu, *tout, *tsT;
+};
 
 // token-major tensor: dense [B, T, H, X] or packed [Ttot, H, X] / [1, Ttot, H, X];
 // beta drops the last dimension.
@@ -269,71 +419,6 @@ kda_status_t check_out_norm(const kda_options_t *o, const kda_tensor_t *out, int
     return KDA_OK;
 }
 
-// ------------------------------------------------------------------ environment
-// KDA_LOG=1: every plan to stderr.  KDA_CHECK=1: cu_seqlens checked on the device before
-// anything else is launched (one small kernel, a stream sync and a 4-byte read back).
-bool env_on(const char *name)
-{
-    const char *v = getenv(name);
-    return v && *v && strcmp(v, "0") != 0;
-}
-
-std::mutex g_check_mu;                 // held for a whole check: one flag buffer per device
-std::vector<int32_t *> g_check_flag;   // per device, allocated on first use
-
-// The KDA_CHECK=1 device checks, before anything else of the call is enqueued: cu_seqlens
-// (when given: cu[0] == 0, non-decreasing, cu[N] == T_tot), the values of g (when given:
-// within [g.lo, g.hi], NaN refused) and decode's slot indices (when given: no two requests
-// name the same slot in [0, P)).  Zeroes three flags, runs the checks, reads the flags back
-// and synchronises the stream; returns KDA_ERR_SHAPE, KDA_ERR_RANGE or KDA_ERR_ALIAS.
-struct DeviceChecks {
-    const int32_t *cu = nullptr;
-    int64_t N = 0, Ttot = 0;
-    bool check_g = false;
-    kda::CheckG g{};
-    const int32_t *slots = nullptr;
-    int64_t R = 0, P = 0;
-};
-
-// flags: device memory for the three flags, or NULL for the library's own buffer (allocated on
-// a device's first check).
-kda_status_t run_device_checks(const DeviceChecks &c, hipStream_t st, int32_t *flags)
-{
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    // the lock covers the launches and the read-back, so that checks on other streams of the
-    // device never write the flags in between
-    std::lock_guard<std::mutex> lk(g_check_mu);
-    int32_t *flag = flags;
-    if (!flag) {
-        if ((int)g_check_flag.size() <= dev) g_check_flag.resize(dev + 1, nullptr);
-        if (!g_check_flag[dev] && (e = hipMalloc(&g_check_flag[dev], 256)) != hipSuccess) {
-            g_check_flag[dev] = nullptr;
-            return hip_fail(e, "device check buffer");
-        }
-        flag = g_check_flag[dev];
-    }
-    int32_t h[3] = {0, 0, 0};
-    if ((e = hipMemsetAsync(flag, 0, sizeof(h), st)) != hipSuccess) return hip_fail(e, "device check reset");
-    if (c.cu && (e = kda::launch_check_cu(c.cu, (int32_t)c.N, c.Ttot, flag, st)) != hipSuccess)
-        return hip_fail(e, "cu_seqlens check");
-    if (c.check_g && (e = kda::launch_check_g(c.g, flag + 1, st)) != hipSuccess) return hip_fail(e, "g range check");
-    if (c.slots && (e = kda::launch_check_slots(c.slots, (int32_t)c.R, (int32_t)c.P, flag + 2, st)) != hipSuccess)
-        return hip_fail(e, "slot check");
-    if ((e = hipMemcpyAsync(h, flag, sizeof(h), hipMemcpyDeviceToHost, st)) != hipSuccess ||
-        (e = hipStreamSynchronize(st)) != hipSuccess)
-        return hip_fail(e, "device check read-back");
-    if (h[0]) return fail(KDA_ERR_SHAPE, "cu_seqlens is not an offset array (cu[0] == 0, non-decreasing, cu[N] == %lld)",
-                          (long long)c.Ttot);
-    if (h[1]) {
-        if (c.g.lo == -INFINITY) return fail(KDA_ERR_RANGE, "g (logits) holds NaN");
-        return fail(KDA_ERR_RANGE, "g holds values outside [%g, %g] (or NaN)", (double)c.g.lo, (double)c.g.hi);
-    }
-    if (h[2]) return fail(KDA_ERR_ALIAS, "two requests name the same state slot with the state update on");
-    return KDA_OK;
-}
-
 // The g view of a token-major problem for the range check: raw log decays must lie in the
 // range the kernels are guaranteed on, [-5, 0]; logits (gate_act) may be anything but NaN.
 kda::CheckG g_view(const kda_tensor_t *g, int64_t rows, int64_t rows_per_b, int64_t sb, int64_t st, int64_t sh,
@@ -361,21 +446,11 @@ struct Plan {
                                 // workspace that holds everything before them runs uncapped
 };
 
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-
 // Capped concurrency: on MI355X the chunk kernel's step time stays within 6% of its low-load
 // value up to about 160 concurrent chains (dense 4,096-token chains: 128 -> 2.00 us, 160 ->
 // 2.04, 192 -> 2.26, 256 -> 2.67 us per step).
 constexpr int64_t kCapChains = 160;
 std::atomic<uint32_t> g_cap_epoch{0};
-
-int device_cus()
-{
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return 256;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) return 256;
-    return cus;
-}
 
 // Segment count from a cost model in units of one chunk step of a launch that leaves most CUs
 // idle (~2.07 us on MI355X).  One segment: C + 3 steps (the longest chain's chunks and the pass's
@@ -551,50 +626,6 @@ kda_status_t make_plan(const Problem &P, const kda_options_t *o, Plan &pl, size_
     return KDA_OK;
 }
 
-// ------------------------------------------------------------- profiling
-struct ProfRec {
-    const char *name;
-    hipEvent_t a, b;
-};
-std::mutex g_prof_mu;
-std::vector<ProfRec> g_prof;                         // launches recorded since the last read
-std::vector<std::pair<hipEvent_t, hipEvent_t>> g_prof_pool;   // idle event pairs
-bool g_prof_on = false;
-
-// Event pairs come from a pool that profiling's enable call fills, so that a timed launch
-// costs two event records and no event creation.
-hipError_t prof_pair(hipEvent_t &a, hipEvent_t &b)
-{
-    if (!g_prof_pool.empty()) {
-        a = g_prof_pool.back().first;
-        b = g_prof_pool.back().second;
-        g_prof_pool.pop_back();
-        return hipSuccess;
-    }
-    hipError_t e = hipEventCreate(&a);
-    if (e == hipSuccess) e = hipEventCreate(&b);
-    return e;
-}
-
-template <typename F>
-hipError_t timed(const char *name, hipStream_t st, F &&launch)
-{
-    if (!g_prof_on) return launch();
-    ProfRec r{name, nullptr, nullptr};
-    hipError_t e;
-    {
-        std::lock_guard<std::mutex> lk(g_prof_mu);
-        if ((e = prof_pair(r.a, r.b)) != hipSuccess) return e;
-    }
-    if ((e = hipEventRecord(r.a, st)) != hipSuccess) return e;
-    e = launch();
-    if (e != hipSuccess) return e;
-    if ((e = hipEventRecord(r.b, st)) != hipSuccess) return e;
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof.push_back(r);
-    return hipSuccess;
-}
-
 // --------------------------------------------------------------- enqueue
 // check_flags: where the KDA_CHECK=1 device checks keep their flags (NULL: the library's own
 // buffer, allocated on a device's first check).
@@ -729,19 +760,6 @@ kda_status_t run(const Problem &P, const Plan &pl, const kda_options_t *o, void 
     return KDA_OK;
 }
 
-// kda_prefill's workspace cache: one buffer per (device, stream), so calls on different
-// streams never share memory, and a buffer is only replaced after its own stream has
-// finished with it.  The lock is held until the call has enqueued its kernels: a call
-// from another thread on the same stream that grows the buffer then waits for them.
-std::mutex g_ws_mu;
-struct CachedWs {
-    int dev = 0;
-    void *stream = nullptr;
-    void *p = nullptr;
-    size_t bytes = 0;
-};
-std::vector<CachedWs> g_ws;
-
 // ------------------------------------------------------ the no-alloc entry point's scratch
 // kda_prefill_noalloc keeps its workspace in this fixed array: KDA_NOALLOC_SCRATCH_BYTES for the
 // plan, then 256 bytes for the KDA_CHECK=1 flags.  Every GPU the library runs on holds its own
@@ -830,35 +848,11 @@ kda_status_t kda_prefill(const kda_tensor_t *q, const kda_tensor_t *k, const kda
     Plan pl;
     if ((st = make_plan(P, nullptr, pl))) return st;
     if (pl.bytes == 0) return run(P, pl, nullptr, nullptr, 0, (hipStream_t)stream);
-    {
-        int dev = 0;
-        hipError_t e = hipGetDevice(&dev);
-        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-        std::lock_guard<std::mutex> lk(g_ws_mu);
-        CachedWs *cp = nullptr;
-        for (CachedWs &x : g_ws)
-            if (x.dev == dev && x.stream == stream) cp = &x;
-        if (!cp) {
-            g_ws.push_back(CachedWs{dev, stream, nullptr, 0});
-            cp = &g_ws.back();
-        }
-        CachedWs &c = *cp;
-        if (c.bytes < pl.bytes) {
-            if (c.p) {
-                if ((e = hipStreamSynchronize((hipStream_t)stream)) != hipSuccess) return hip_fail(e, "workspace sync");
-                e = hipFree(c.p);
-                c.p = nullptr;
-                c.bytes = 0;
-                if (e != hipSuccess) return hip_fail(e, "workspace free");
-            }
-            if ((e = hipMalloc(&c.p, pl.bytes)) != hipSuccess) {
-                c.p = nullptr;
-                return fail(KDA_ERR_WORKSPACE, "hipMalloc(%zu): %s", pl.bytes, hipGetErrorString(e));
-            }
-            c.bytes = pl.bytes;
-        }
-        return run(P, pl, nullptr, c.p, pl.bytes, (hipStream_t)stream);
-    }
+    struct Call { const Problem *P; const Plan *pl; void *stream; } call{&P, &pl, stream};
+    return with_cached_ws(pl.bytes, stream, [](void *ws, void *arg) {
+        const Call &c = *(const Call *)arg;
+        return run(*c.P, *c.pl, nullptr, ws, c.pl->bytes, (hipStream_t)c.stream);
+    }, &call);
 }
 
 kda_status_t kda_decode(const kda_tensor_t *q, const kda_tensor_t *k, const kda_tensor_t *v, const kda_tensor_t *g,
