@@ -117,8 +117,8 @@ struct QkNormParams {
     float eps, inv_d;          // inv_d: 1 / D (rms) or 1 (l2)
     int32_t rot, offset;
     float scale;
-    int32_t tile;              // tokens per workgroup
-    int32_t splits;            // workgroups that share a token tile's rows
+    int32_t batched;           // tokens are [B, T]: the batch strides matter
+    int32_t splits;            // waves that share a token's rows
 };
 hipError_t launch_qk_norm(const QkNormParams &p, bool io_f32, int vec, bool interleaved, hipStream_t st);
 
@@ -143,7 +143,7 @@ struct SsmParams {
     int32_t heads_per_wg;
     int32_t wide;              // x, z, B, C rows are 16-byte aligned (else 8-byte, bf16)
     float *ws_state;           // [slots][H][N x P]
-    float *ws_decay;           // [slots][H]: sum of A step over the segment
+    double *ws_decay;          // [slots][H]: sum of A step over the segment, in powers of two
 };
 // states_only: the end state of every segment from a zero start, and its decay (pass 1);
 // otherwise the outputs.

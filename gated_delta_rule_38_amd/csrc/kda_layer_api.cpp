@@ -451,13 +451,12 @@ kda_status_t qk_norm(const kda_tensor_t *q, const kda_tensor_t *k, const kda_ten
     const int vec = !f32 && D % 8 == 0 && aligned_to(q, 8) && aligned_to(k, 8) && aligned_to(qo, 8) && aligned_to(ko, 8) ? 8 : 4;
     int lanes = 1;
     while (lanes * vec < D) lanes *= 2;
-    const int64_t per = 256 / lanes;                       // rows of one round of a workgroup
-    p.tile = 4;
-    while (p.tile > 1 && (tokens / p.tile < 1024)) p.tile /= 2;
+    const int64_t rounds = (heads + 64 / lanes - 1) / (64 / lanes);
+    // one wave a token; with fewer tokens than fill the chip, several share a token's heads
     p.splits = 1;
-    while ((tokens + p.tile - 1) / p.tile * p.splits < 1024 && p.splits * per < p.tile * heads) p.splits *= 2;
-    if ((tokens + p.tile - 1) / p.tile * p.splits > (int64_t)INT32_MAX)
-        return fail(KDA_ERR_UNSUPPORTED, "too many workgroups for one launch");
+    while (tokens * p.splits < 4096 && p.splits < rounds) p.splits *= 2;
+    if (tokens * p.splits / 4 > (int64_t)INT32_MAX - 1) return fail(KDA_ERR_UNSUPPORTED, "too many workgroups for one launch");
+    p.batched = lead == 2;
     hipError_t e = timed("kda_qk_norm", st, [&] {
         return kda::launch_qk_norm(p, f32, vec, o->rotary_layout == KDA_ROTARY_INTERLEAVED, st);
     });
@@ -529,7 +528,7 @@ void ssm_plan(Ssm &s, const kda_ssm_options_t *o)
     }
     s.slots = s.L.dense ? s.L.N * std::max<int64_t>(1, (s.L.T + s.seg - 1) / s.seg) : s.L.tokens / s.seg + s.L.N;
     s.off_decay = align256((size_t)s.slots * s.H * s.N * s.P * 4);
-    s.bytes = s.off_decay + align256((size_t)s.slots * s.H * 4);
+    s.bytes = s.off_decay + align256((size_t)s.slots * s.H * 8);
 }
 
 kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_tensor_t *A, const kda_tensor_t *B,
@@ -574,6 +573,10 @@ kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_
     if (sT) KDA_TRY(ssm_state(sT, "final_state", s.L.N, s.H, s.N, s.P));
     for (const kda_tensor_t *t : {x, B, C, (const kda_tensor_t *)out, s.tz})
         if (!aligned_to(t, 4)) return fail(KDA_ERR_LAYOUT, "x, B, C, z and out need 4-element-aligned base addresses and strides");
+    // the kernel addresses a chunk of each with 32-bit byte offsets from its first row
+    for (int64_t stride : {s.x.st, s.B.st, s.C.st, s.z.st, s.out.st})
+        if (stride > ((int64_t)1 << 31) / (kda::SSM_CHUNK * 4) - 256)
+            return fail(KDA_ERR_UNSUPPORTED, "token strides must stay below 2^24 - 256 elements");
     const Named ins[] = {{x, "x"}, {dt, "dt"}, {A, "A"}, {B, "B"}, {C, "C"}, {s0, "initial_state"}, {cu, "cu_seqlens"},
                          {s.tD, "D"}, {s.tbias, "dt_bias"}, {s.tz, "z"}};
     KDA_TRY(no_overlap(out, "out", ins));
@@ -614,9 +617,9 @@ kda_status_t ssm_run(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_te
     p.dt_bf16 = dt->dtype == KDA_BF16; p.softplus = s.softplus;
     p.s0_bf16 = s0 && s0->dtype == KDA_BF16; p.sT_bf16 = sT && sT->dtype == KDA_BF16;
     p.seg = (int32_t)s.seg; p.slots = (int32_t)s.slots; p.wg_per_slot = (int32_t)s.wps; p.heads_per_wg = s.hpw;
-    p.wide = aligned_to(x, 8) && aligned_to(B, 8) && aligned_to(C, 8) && aligned_to(s.tz, 8);
+    p.wide = aligned_to(x, 8) && aligned_to(B, 8) && aligned_to(C, 8) && aligned_to(s.tz, 8) && aligned_to(out, 8);
     p.ws_state = (float *)ws;
-    p.ws_decay = ws ? (float *)((char *)ws + s.off_decay) : nullptr;
+    p.ws_decay = ws ? (double *)((char *)ws + s.off_decay) : nullptr;
     const bool f32 = x->dtype == KDA_F32;
     hipError_t e;
     if (s.seg) {

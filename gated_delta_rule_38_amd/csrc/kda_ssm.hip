@@ -2,25 +2,33 @@
 //     S_t = e^{a_t} S_{t-1} + step_t B_t x_t^T,   y_t = S_t^T C_t + D x_t,   out = y silu(z),
 // a_t = A step_t, one decay per head and token, S an N x P matrix per head.
 //
-// Chunks of L = 32 tokens, with c_i = a_1 + ... + a_i inside the chunk:
-//     Y^T = X^T (B C^T o E) + (S^T C^T) diag(e^{c_i}),   E_ji = step_j e^{c_i - c_j} for j <= i, else 0
-//     S  <- e^{c_L} S + B^T diag(step_j e^{c_L - c_j}) X
-// every exponent a difference taken directly (no factor can overflow when a <= 0); the ones of
-// the state use sums from the chunk's end, so that the weights near 1 keep full precision.
+// Chunks of L = 32 tokens.  With c_i the sum of a up to token i since a reference token and the
+// state kept in units of the reference, S = e^{c} Z, a chunk is
+//     Y^T = [Z^T C^T + (X diag(g))^T (B C^T, j <= i)] diag(e^{c_i}),   g_j = step_j e^{-c_j}
+//     Z  <- Z + B^T diag(g) X
+// so one weighted copy of x serves both products, the decay matrix is never formed and the state
+// is not touched by decays.  The reference moves (Z <- e^{c} Z) before e^{-c} could leave 2^LIMIT;
+// a chunk that decays by more than that on its own takes the direct form, every exponent a
+// difference: Y^T = (Z^T C^T) diag(e^{c_i}) + X^T (B C^T o step_j e^{c_i - c_j}, j <= i) and
+// Z <- e^{c_L} Z + B^T diag(step_j e^{c_L - c_j}) X.  c is summed in 64 bits: weights and decays
+// then carry full 32-bit precision however far the reference is.
 //
-// One wave owns 32 value columns of one head's state, in MFMA 32x32 accumulators for the whole
-// chain, and forms everything those columns need: B C^T (32 x 32, 16 FMAs' worth of matrix time a
-// wave, cheaper than sharing it through LDS and a barrier), Y^T and the state update.  The
-// accumulator layout (lane = column, registers = rows) is the next product's operand as it
-// stands: B C^T becomes the B operand of X^T (..), and S the A operand S^T.  B and C rows are
-// shared by the workgroup's waves (two heads of a group for P = 64) in LDS, double-buffered, one
-// barrier a chunk; x and z tiles belong to one wave each and need none.
-// LDS rows are permuted in units of 4 elements so that both the row reads (32 rows, 8 bytes) and
-// the transposed reads (4 rows, 32 bytes a 16-lane group) touch every bank once.
+// One wave owns 16 value columns of one head's state, in MFMA 16x16 accumulators for the whole
+// chain (32 registers for N = 128), so that four waves share a SIMD and one wave's conversions and
+// exponentials run under another's matrix products.  The accumulator layout (lane = column,
+// registers = rows) is the next product's operand as it stands: Z feeds Z^T C^T, and B C^T, formed
+// once a chunk and workgroup, feeds every wave's X^T (..) through 2 KB of LDS.  A workgroup is
+// 8 waves (two heads of a group for P = 64, one for P = 128) over double-buffered tiles of B, C, x
+// and z; two barriers a chunk.  Steps, sums, weights and decays of 8 (chunk, head) pairs are formed
+// at a time, one pair in each half of four waves.
+// State rows are numbered so that the 8 registers of a lane's two tiles are 8 consecutive channels
+// (the transposed reads fetch columns in that order), which makes every row access 16 bytes.  In
+// LDS the 8-element units of a row are permuted by the row number so that row reads (one unit of
+// each row) touch every bank once, and transposed reads (4 rows, 4 neighbouring units) twice.
 //
 // Precision on bf16 data: x, B, C enter exactly; weighted x is split into three bf16 parts (24
-// bits) for the state update, so states carry fp32 precision; the decayed B C^T and the copy of S
-// that only feed the bf16 output are rounded to bf16 once (2^-9 relative each).
+// bits) for the state update, so states carry fp32 precision, and two of them (16 bits) feed the
+// output; B C^T and the copy of the state that only feed the bf16 output are rounded to bf16 once.
 //
 // Sequences too few to fill the chip are cut into segments of equal length: pass 1 runs every
 // segment but the last of its sequence from a zero state (state update only), a scan turns the end
@@ -34,93 +42,104 @@ namespace kda {
 namespace ssm {
 
 constexpr int L = SSM_CHUNK;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Physical unit of logical unit u (4 elements) of row r in a tile of U units a row.  32 row reads
-// at one u, and 4 rows x 8 units of a transposed read, each spread over all 64 banks (bf16).
-template <int U>
-__device__ __forceinline__ int unit(int r, int u)
+// Element offset of unit u (8 elements) of row r in a tile of COLS columns.
+template <int COLS>
+__device__ __forceinline__ int unit_at(int r, int u)
 {
-    if constexpr (U == 32) return u ^ (((r & 3) << 3) | ((r >> 2) & 7));
-    else if constexpr (U == 16) return u ^ ((((r >> 1) & 1) << 3) | ((r >> 2) & 7));
-    else return u ^ ((r >> 2) & 7);
+    const int f = COLS == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    return r * COLS + ((u ^ f) << 3);
 }
 
-// 4 consecutive elements of row r, logical unit u
-template <typename ET, int U>
-__device__ __forceinline__ typename Vec4<ET>::raw lds_unit(const ET *tile, int r, int u)
-{
-    return Vec4<ET>::load(tile + (r * U + unit<U>(r, u)) * 4);
-}
+// The offsets one lane needs in a tile of COLS columns (l16 = lane % 16, g = lane / 16).
+template <typename ET, int COLS>
+struct Rows {                   // row l16 (+ 16 t): units g + 4 a
+    int base;
+    __device__ __forceinline__ explicit Rows(int lane) : base(unit_at<COLS>(lane & 15, lane >> 4)) {}
+    // (the permutation is an exclusive or, the same for rows 16 apart)
+    __device__ __forceinline__ int at(int t, int a) const { return (base ^ (a << 5)) + t * 16 * COLS; }
+};
 
-// operand fragment: row r, elements 16 ks + 4 g + 0..3 and 16 ks + 8 + 4 g + 0..3
-template <typename ET, int U>
-__device__ __forceinline__ void row_frag(Frag8<ET> &f, const ET *tile, int r, int ks, int g)
-{
-    f.load44(tile + (r * U + unit<U>(r, 4 * ks + g)) * 4, tile + (r * U + unit<U>(r, 4 * ks + 2 + g)) * 4);
-}
-
-// operand fragment of the transpose: element k of lane l is tile[row 16 ks + 4 g + k (k < 4) or
-// 16 ks + 8 + 4 g + k - 4][32 m + l % 32]
-template <typename ET, int U>
-__device__ __forceinline__ void col_frag(Frag8<ET> &f, const ET *tile, int ks, int m, int lane)
-{
-    const int g = lane >> 5;
-    if constexpr (sizeof(ET) == 2) {
-        const int r = 16 * ks + 4 * g + ((lane & 15) >> 2), u = 8 * m + 4 * ((lane >> 4) & 1) + (lane & 3);
-        f.load44_tr(tile + (r * U + unit<U>(r, u)) * 4, tile + ((r + 8) * U + unit<U>(r + 8, u)) * 4);
-    } else {
-        const int c = 32 * m + (lane & 31);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = 16 * ks + 4 * g + (k & 3) + 8 * (k >> 2);
-            f.v[k] = tile[(r * U + unit<U>(r, c >> 2)) * 4 + (c & 3)];
+// The transposed operand of 32 tokens: element k of lane l is token 4 g + k (k < 4) or 16 + 4 g + k - 4.
+// SPREAD: lane l16 stands for channel 8 (l16 / 4) + l16 % 4 (+ 4 for the odd tile) of 32, else for
+// column l16.
+template <typename ET, int COLS, bool SPREAD>
+struct Cols {
+    int base;
+    __device__ __forceinline__ explicit Cols(int lane, int first)
+    {
+        const int g = lane >> 4;
+        if constexpr (sizeof(ET) == 2) {
+            // the transposing read: this lane addresses word l16 % 4 of row l16 / 4
+            const int r = 4 * g + ((lane & 15) >> 2), wd = lane & 3;
+            base = SPREAD ? unit_at<COLS>(r, wd) : unit_at<COLS>(r, (first >> 3) + (wd >> 1)) + (wd & 1) * 4;
+        } else {
+            const int c = SPREAD ? 8 * ((lane & 15) >> 2) + (lane & 3) : first + (lane & 15);
+            base = unit_at<COLS>(4 * g, c >> 3) + (c & 7);
         }
     }
-}
+    // SPREAD: channels 32 a ..; odd: their upper fours
+    __device__ __forceinline__ void get(Frag8<ET> &f, const ET *tile, int a, int odd) const
+    {
+        const ET *t = tile + (base ^ (a << 5)) + 4 * odd;
+        if constexpr (sizeof(ET) == 2) {
+            f.load44_tr(t, t + 16 * COLS);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                // rows 1 .. 3 of a group of four: their permutations differ in the bits of row % 4
+                const int d = k & 3, x = COLS == 128 ? d << 2 : ((d >> 1) & 1) << 2;
+                f.v[k] = tile[(((base ^ (a << 5)) ^ (x << 3)) + 4 * odd) + (d + 16 * (k >> 2)) * COLS];
+            }
+        }
+    }
+};
 
-// A tile of 32 rows of `cols` elements on its way from HBM to LDS: `per` threads of index t move
-// 8 elements (bf16) or 4 (fp32) each, K times.
-template <typename ET, int COLS, int PER>
+// A tile of 32 rows of COLS elements on its way from HBM to LDS: PER threads move 8 elements (bf16)
+// or 4 (fp32) each, K times.  The columns belong to heads of PC columns that lie `head` elements
+// apart.
+template <typename ET, int COLS, int PER, int PC>
 struct TileRegs {
     static constexpr int EPV = sizeof(ET) == 2 ? 8 : 4;      // elements of a 16-byte piece
-    static constexpr int PIECES = L * COLS / EPV, K = PIECES / PER, PPR = COLS / EPV;
-    static_assert(PIECES % PER == 0, "whole pieces");
-    uint4 v[K];
-    // rows past `rows` become zeros.  wide: every piece is 16-byte aligned; else 8-byte (bf16)
-    __device__ __forceinline__ void load(const ET *p, int64_t stride, int rows, int t, bool wide)
+    static constexpr int PIECES = L * COLS / EPV, USED = PER < PIECES ? PER : PIECES;     // threads that move any
+    static constexpr int K = PIECES / USED, PPR = COLS / EPV, ROWS = USED / PPR;
+    static_assert(PIECES % USED == 0 && USED % PPR == 0, "whole pieces, whole rows");
+    u32x4 v[K];
+    uint32_t off[K];            // byte offsets from the chunk's first row
+    // rows past the last one repeat it: their step is 0, so they weigh nothing
+    __device__ __forceinline__ void offsets(int64_t stride, int64_t head, int heads, int rows, int t)
     {
+        const int c = t % PPR * EPV;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            off[k] = ((uint32_t)min(t / PPR + k * ROWS, rows - 1) * (uint32_t)stride + (uint32_t)min(c / PC, heads - 1) * (uint32_t)head +
+                      (uint32_t)(c % PC)) * (uint32_t)sizeof(ET);
+    }
+    // WIDE: every piece is 16-byte aligned; else 8-byte (bf16)
+    template <bool WIDE>
+    __device__ __forceinline__ void load(const ET *p, int t)
+    {
+        if (USED < PER && t >= USED) return;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int piece = t + k * PER, r = piece / PPR, c = piece % PPR;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows) {
-                const ET *s = p + r * stride + c * EPV;
-                if (wide || sizeof(ET) == 4) {
-                    x = *(const uint4 *)s;
-                } else {
-                    const uint2 a = *(const uint2 *)s, b = *(const uint2 *)(s + 4);
-                    x = make_uint4(a.x, a.y, b.x, b.y);
-                }
+            const char *s = (const char *)p + off[k];
+            if constexpr (WIDE || sizeof(ET) == 4) {
+                v[k] = *(const u32x4 *)s;
+            } else {
+                const uint2 a = *(const uint2 *)s, b = *(const uint2 *)(s + 8);
+                v[k] = u32x4{a.x, a.y, b.x, b.y};
             }
-            v[k] = x;
         }
     }
     __device__ __forceinline__ void store(ET *tile, int t) const
     {
-        constexpr int U = COLS / 4;
+        if (USED < PER && t >= USED) return;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int piece = t + k * PER, r = piece / PPR, c = piece % PPR;
-            if constexpr (sizeof(ET) == 4) {
-                *(uint4 *)(tile + (r * U + unit<U>(r, c)) * 4) = v[k];
-            } else {
-                // the two units of a piece stay neighbours, in one order or the other
-                const int a = unit<U>(r, 2 * c);
-                const bool odd = a & 1;
-                const uint4 x = v[k];
-                *(uint4 *)(tile + (r * U + (a & ~1)) * 4) =
-                    make_uint4(odd ? x.z : x.x, odd ? x.w : x.y, odd ? x.x : x.z, odd ? x.y : x.w);
-            }
+            const int r = t / PPR + k * ROWS, c = t % PPR;
+            // a piece is a unit (bf16) or half of one (fp32)
+            *(u32x4 *)(tile + (sizeof(ET) == 2 ? unit_at<COLS>(r, c) : unit_at<COLS>(r, c >> 1) + 4 * (c & 1))) = v[k];
         }
     }
 };
@@ -146,10 +165,67 @@ __device__ __forceinline__ void split3(const float (&f)[8], Frag8<bf16> (&o)[3])
     }
 }
 
-// softplus without cancellation for steps far below 1
+// 2^x of a 64-bit exponent, to 32-bit precision: the whole part goes into the exponent bits.
+__device__ __forceinline__ float exp2_of(double x)
+{
+    x = fmin(fmax(x, -4096.), 4096.);
+    const double n = __builtin_rint(x);
+    return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp64(double x)      // lanes without a source read 0
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Inclusive sum over the lanes of each 32-lane half: shifts within 16-lane rows, then lane 15 of
+// the row before.
+__device__ __forceinline__ double prefix32(double x)
+{
+    x += dpp64<0x111, 0xf>(x);
+    x += dpp64<0x112, 0xf>(x);
+    x += dpp64<0x114, 0xf>(x);
+    x += dpp64<0x118, 0xf>(x);
+    x += dpp64<0x142, 0xa>(x);
+    return x;
+}
+
+// The reference moves before a weight could pass 2^LIMIT (and a decay fall under 2^-LIMIT): products
+// of x, B and C up to 2^31 still fit an fp32 number, and the direct form, slower by a third, is left
+// to chunks that decay by more than 2^-96.
+constexpr double LIMIT = 96.;
+
+// softplus(v) = max(v, 0) + log(1 + e^{-|v|}) without cancellation for steps far below 1: log(1 + t) is
+// 2 atanh(s), s = t / (2 + t) <= 1/3, by its odd power series (the first term left out is under
+// 2^-27 of the sum).
 __device__ __forceinline__ float step_of(float v, int softplus)
 {
-    return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+    if (!softplus) return v;
+    const float t = __builtin_amdgcn_exp2f(-fabsf(v) * LOG2E), d = 2.f + t;
+    float r = __builtin_amdgcn_rcpf(d);
+    r = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.f), r);
+    const float s = t * r, q = s * s;
+    float a = 1.f / 15.f;
+    a = __builtin_fmaf(a, q, 1.f / 13.f);
+    a = __builtin_fmaf(a, q, 1.f / 11.f);
+    a = __builtin_fmaf(a, q, 1.f / 9.f);
+    a = __builtin_fmaf(a, q, 1.f / 7.f);
+    a = __builtin_fmaf(a, q, 1.f / 5.f);
+    a = __builtin_fmaf(a, q, 1.f / 3.f);
+    a = __builtin_fmaf(a * q, s, s);
+    return fmaxf(v, 0.f) + 2.f * a;
+}
+
+// The same value, but not one the compiler can compute before a loop: what depends on it stays where
+// it is used instead of holding registers through the loop.
+__device__ __forceinline__ int here(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 struct Place {
@@ -206,29 +282,37 @@ __device__ __forceinline__ Place place(const SsmParams &p, int slot)
     return w;
 }
 
-// Offset of accumulator registers 4 q .. 4 q + 3 of tile m of a state, in the workspace's order
-// (the order a wave holds it in, 16 bytes a lane).
+// Offset of tile m of a state's 16-column slab, in the workspace's order (the order a wave holds it
+// in, 16 bytes a lane).
 template <int P, int N>
-__device__ __forceinline__ int ws_index(int slab, int m, int q, int lane)
-{
-    return ((slab * (N / 32) + m) * 4 + q) * 256 + lane * 4;
-}
+__device__ __forceinline__ int ws_index(int slab, int m, int lane) { return ((slab * (N / 16) + m) * 64 + lane) * 4; }
 
-template <typename ET, int P, int N, int HPW, bool OUT>
-__global__ __launch_bounds__(HPW * P * 2, 2) void ssm_kernel(const SsmParams p)
+// Channel of register r of tile m (lane group g = lane / 16).
+__device__ __forceinline__ int row_of(int m, int g, int r) { return 32 * (m >> 1) + 8 * g + 4 * (m & 1) + r; }
+
+// GATED: z is given.
+template <typename ET, int P, int N, int HPW, bool OUT, bool GATED>
+__global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kernel(const SsmParams p)
 {
-    constexpr int NW = HPW * P / 32, NT = NW * 64;      // waves, threads
-    constexpr int SLABS = P / 32, NM = N / 32, U = N / 4;
+    constexpr int NW = HPW * P / 16, NT = NW * 64;      // waves, threads
+    constexpr int SLABS = P / 16, NM = N / 16, NA = N / 32, XC = HPW * P;
+    constexpr bool BF = sizeof(ET) == 2;
+    constexpr int PARTS = BF ? 3 : 1;                   // of weighted x
+    constexpr int GC = 8 / HPW;                         // chunks of a group
     __shared__ __attribute__((aligned(16))) ET sB[2][L * N];
     __shared__ __attribute__((aligned(16))) ET sC[OUT ? 2 : 1][OUT ? L * N : 4];
-    __shared__ __attribute__((aligned(16))) ET sX[NW][L * 32];
-    __shared__ __attribute__((aligned(16))) ET sZ[OUT ? NW : 1][OUT ? L * 32 : 4];
-    // c log2 e, step, state weight; on fp32 data also the low part of c: after a large decay the
-    // differences c_i - c_j of two 32-bit sums would keep too few digits for an fp32 output
-    constexpr bool FINE = sizeof(ET) == 4;
-    __shared__ __attribute__((aligned(16))) float sAux[NW][FINE ? 4 : 3][L];
+    __shared__ __attribute__((aligned(16))) ET sX[2][L * XC];
+    __shared__ __attribute__((aligned(16))) ET sZ[GATED ? 2 : 1][GATED ? L * XC : 4];
+    __shared__ __attribute__((aligned(16))) ET sM[OUT ? L * L : 4];     // C B^T, j <= i: row i, units of 4 j
+    // of a group's chunks and heads, for each token: step, sum of a, weight of x, decay of y
+    __shared__ __attribute__((aligned(16))) float sStep[2][GC][HPW][L], sWt[2][GC][HPW][L], sEi[OUT ? 2 : 1][GC][HPW][L];
+    __shared__ __attribute__((aligned(16))) float2 sSum[2][GC][HPW][L];
+    // and for each chunk: the factor the state takes before it, c after it, whether it is direct
+    __shared__ double sBase[2][GC][HPW];
+    __shared__ float sScale[2][GC][HPW];
+    __shared__ int sDirect[2][GC][HPW];
 
-    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, g = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x / p.wg_per_slot, wgi = blockIdx.x % p.wg_per_slot;
     const Place w = place(p, slot);
@@ -236,220 +320,322 @@ __global__ __launch_bounds__(HPW * P * 2, 2) void ssm_kernel(const SsmParams p)
     // heads: this workgroup's HPW heads of one group (a wave past the group's last head repeats it
     // and stores nothing)
     const int hg = p.H / p.G, wpg = (hg + HPW - 1) / HPW, grp = wgi / wpg;
-    const int hi = (wgi % wpg) * HPW + wave / SLABS, slab = wave % SLABS;
-    const bool live = hi < hg;
-    const int h = grp * hg + min(hi, hg - 1);
+    const int h0 = grp * hg + (wgi % wpg) * HPW, heads = min(HPW, (grp + 1) * hg - h0);
+    const int wh = wave / SLABS, slab = wave % SLABS;
+    const bool live = wh < heads;
+    const int h = h0 + min(wh, heads - 1);
 
     const int64_t seq = p.cu ? 0 : w.n;
-    const ET *x = (const ET *)p.x + seq * p.x_sb + w.tok * p.x_st + h * p.x_sh + slab * 32;
-    const ET *Bp = (const ET *)p.B + seq * p.B_sb + w.tok * p.B_st + grp * p.B_sg;
-    const ET *Cp = (const ET *)p.C + seq * p.C_sb + w.tok * p.C_st + grp * p.C_sg;
-    const ET *z = p.z ? (const ET *)p.z + seq * p.z_sb + w.tok * p.z_st + h * p.z_sh + slab * 32 : nullptr;
-    ET *o = (ET *)p.o + seq * p.o_sb + w.tok * p.o_st + h * p.o_sh + slab * 32;
-    const int64_t dt0 = seq * p.dt_sb + w.tok * p.dt_st + h * p.dt_sh;
-    const float a2 = p.A[h] * LOG2E, bias = p.dt_bias ? p.dt_bias[h] : 0.f, skip = p.Dv ? p.Dv[h] : 0.f;
+    const float skip = p.Dv ? p.Dv[h] : 0.f;
+    const Rows<ET, N> rn(lane);
+    const Cols<ET, N, true> cn(lane, 0);
+    const Cols<ET, XC, false> cx(lane, wh * P + slab * 16);
+    // row l16, columns 4 g .. 4 g + 3 of this wave's slab of x and z
+    const int xrow = unit_at<XC>(l16, (wh * P + slab * 16 + 4 * g) >> 3) + 4 * (g & 1);
+    // row l16 of M: units of 4 j, permuted by the row
+    auto m_at = [&](int i, int u) { return i * L + ((u ^ ((i >> 2) & 7)) << 2); };
 
     // start state
-    f32x16 S[NM];
+    f32x4 S[NM];
     float *ws = p.seg ? p.ws_state + ((int64_t)slot * p.H + h) * (N * P) : nullptr;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
         if (OUT && p.seg) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 v = *(const float4 *)(ws + ws_index<P, N>(slab, m, q, lane));
-                S[m][4 * q] = v.x; S[m][4 * q + 1] = v.y; S[m][4 * q + 2] = v.z; S[m][4 * q + 3] = v.w;
-            }
+            S[m] = *(const f32x4 *)(ws + ws_index<P, N>(slab, m, lane));
         } else if (OUT && p.s0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = 32 * m + 8 * (e >> 2) + 4 * g + (e & 3);
-                S[m][e] = ld_any(p.s0, w.n * p.s0_sn + h * p.s0_sh + row * p.s0_sr + slab * 32 + l32, p.s0_bf16);
-            }
+            for (int r = 0; r < 4; ++r)
+                S[m][r] = ld_any(p.s0, w.n * p.s0_sn + h * p.s0_sh + row_of(m, g, r) * p.s0_sr + slab * 16 + l16, p.s0_bf16);
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) S[m][e] = 0.f;
+            for (int r = 0; r < 4; ++r) S[m][r] = 0.f;
         }
     }
-
-    TileRegs<ET, N, NT> rB, rC;
-    TileRegs<ET, 32, 64> rX, rZ;
-    float rdt = 0.f;
-    const int nck = (w.len + L - 1) / L;
-    auto load = [&](int c) {
-        const int rows = min(L, w.len - c * L);
-        const int64_t t = (int64_t)c * L;
-        rB.load(Bp + t * p.B_st, p.B_st, rows, tid, p.wide);
-        if constexpr (OUT) rC.load(Cp + t * p.C_st, p.C_st, rows, tid, p.wide);
-        rX.load(x + t * p.x_st, p.x_st, rows, lane, p.wide);
-        if constexpr (OUT)
-            if (z) rZ.load(z + t * p.z_st, p.z_st, rows, lane, p.wide);
-        rdt = l32 < rows ? ld_any(p.dt, dt0 + (t + l32) * p.dt_st, p.dt_bf16) : 0.f;
-    };
-    if (nck > 0) load(0);
-    float total2 = 0.f;         // sum of a over the segment, in powers of two
-    for (int c = 0; c < nck; ++c) {
-        const int rows = min(L, w.len - c * L);
-        ET *tB = sB[c & 1], *tC = sC[OUT ? c & 1 : 0], *tX = sX[wave], *tZ = sZ[OUT ? wave : 0];
-        rB.store(tB, tid);
-        if constexpr (OUT) rC.store(tC, tid);
-        rX.store(tX, lane);
-        if constexpr (OUT)
-            if (z) rZ.store(tZ, lane);
-        // decays of the chunk: token i = lane % 32; tokens past the end have step 0
-        const float step = l32 < rows ? step_of(rdt + bias, p.softplus) : 0.f;
-        const float a = step * a2;
-        typedef std::conditional_t<FINE, double, float> sum_t;
-        sum_t cs = a;
-        float ri = a;
+    auto scale_state = [&](float f) {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const sum_t u = __shfl_up(cs, off, 32);
-            const float d = __shfl_down(ri, off, 32);
-            cs += l32 >= off ? u : (sum_t)0;
-            ri += l32 + off < 32 ? d : 0.f;
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[m][r] *= f;
+    };
+
+    TileRegs<ET, N, NT, N> rB, rC;
+    const int tc = tid ^ (NT / 2);      // (where half the threads move a tile, B and C take one half each)
+    TileRegs<ET, XC, NT, P> rX, rZ;
+    const int nck = (w.len + L - 1) / L;
+    const ET *Bp = (const ET *)p.B + seq * p.B_sb + w.tok * p.B_st + grp * p.B_sg;
+    const ET *Cp = (const ET *)p.C + seq * p.C_sb + w.tok * p.C_st + grp * p.C_sg;
+    const ET *xp = (const ET *)p.x + seq * p.x_sb + w.tok * p.x_st + h0 * p.x_sh;
+    const ET *zp = (const ET *)p.z + seq * p.z_sb + w.tok * p.z_st + h0 * p.z_sh;
+    auto offsets = [&](int rows) {
+        rB.offsets(p.B_st, 0, 1, rows, tid);
+        rX.offsets(p.x_st, p.x_sh, heads, rows, tid);
+        if constexpr (OUT) rC.offsets(p.C_st, 0, 1, rows, tc);
+        if constexpr (GATED) rZ.offsets(p.z_st, p.z_sh, heads, rows, tid);
+    };
+    auto load_as = [&](int c, auto wide) {
+        constexpr bool W = decltype(wide)::value;
+        const int64_t t = (int64_t)c * L;
+        rB.template load<W>(Bp + t * p.B_st, tid);
+        rX.template load<W>(xp + t * p.x_st, tid);
+        if constexpr (OUT) rC.template load<W>(Cp + t * p.C_st, tc);
+        if constexpr (GATED) rZ.template load<W>(zp + t * p.z_st, tid);
+    };
+    auto load = [&](int c) {
+        if (w.len - c * L < L) offsets(w.len - c * L);
+        if (p.wide) load_as(c, std::true_type{});
+        else load_as(c, std::false_type{});
+    };
+
+    // The decays of a group, in halves of waves 0 .. 3: half wave u forms chunk uc of the group for
+    // head uh.  First steps and their sums (a barrier follows before the second part), then the
+    // reference's walk over the group's chunks, the weights and the decays.
+    struct Unit {
+        int c, h, i;            // chunk of the group, head of the workgroup, token
+    };
+    auto unit = [&] {
+        const int t = here(tid), u = t >> 5;
+        return Unit{u / HPW, u % HPW, t & 31};
+    };
+    const bool forms = wave < 4;
+    auto load_dt = [&](int k) {
+        const Unit u = unit();
+        const int t = min((k * GC + u.c) * L + u.i, w.len - 1);
+        const int64_t at = seq * p.dt_sb + (w.tok + t) * p.dt_st + (h0 + min(u.h, heads - 1)) * p.dt_sh;
+        return k * GC < nck ? ld_any(p.dt, at, p.dt_bf16) : 0.f;
+    };
+    auto steps = [&](int k, float raw) {            // tokens past the end: step 0
+        const Unit u = unit();
+        const int hu = h0 + min(u.h, heads - 1);
+        const float step = (k * GC + u.c) * L + u.i < w.len ? step_of(raw + (p.dt_bias ? p.dt_bias[hu] : 0.f), p.softplus) : 0.f;
+        sStep[k & 1][u.c][u.h][u.i] = step;
+        // decays in powers of two; sums in 64 bits, kept as two floats
+        const double cs = prefix32((double)step * ((double)p.A[hu] * 1.4426950408889634));
+        sSum[k & 1][u.c][u.h][u.i] = make_float2((float)cs, (float)(cs - (double)(float)cs));
+    };
+    auto sum_of = [&](float2 v) { return (double)v.x + (double)v.y; };
+    auto weights = [&](int k) {
+        const Unit u = unit();
+        // c at the group's start: the state is 2^base times what S holds
+        double base = k ? sBase[(k - 1) & 1][GC - 1][u.h] : 0.;
+        double mine = 0., after = 0.;
+        float scale = 1.f;
+        bool direct = false;
+        for (int c = 0; c < GC; ++c) {
+            const double tot = sum_of(sSum[k & 1][c][u.h][L - 1]), old = base;
+            const bool d = tot < -LIMIT, move = base + tot < -LIMIT && base != 0.;
+            if (move) base = 0.;
+            if (c == u.c) {
+                mine = base;
+                direct = d;
+                scale = move ? exp2_of(old) : 1.f;
+            }
+            if (!d) base += tot;                    // (a direct chunk leaves S in its own units)
+            if (c == u.c) after = base;
         }
-        const float ci = (float)cs, cl = (float)(cs - (sum_t)ci);       // cl: 0 unless FINE
-        const float tot = __shfl(ci, 31, 32);
-        float rev = __shfl_down(ri, 1, 32);
-        rev = l32 == 31 ? 0.f : rev;                // sum over the tokens after i
-        if (g == 0) {
-            sAux[wave][0][l32] = ci;
-            sAux[wave][1][l32] = step;
-            sAux[wave][2][l32] = step * __builtin_amdgcn_exp2f(rev);
-            if constexpr (FINE) sAux[wave][3][l32] = cl;
+        const double cs = sum_of(sSum[k & 1][u.c][u.h][u.i]);
+        // e^{c_i}, and the weight: e^{-c_j} step_j, or e^{c_L - c_j} step_j
+        const double ce = fmin(fmax(mine + cs, -4096.), 4096.), cr = __builtin_rint(ce);
+        const float cf = (float)(ce - cr);
+        const int ci = (int)cr;
+        if constexpr (OUT) sEi[k & 1][u.c][u.h][u.i] = __builtin_ldexpf(__builtin_amdgcn_exp2f(cf), ci);
+        float wt = __builtin_ldexpf(__builtin_amdgcn_exp2f(-cf), -ci);
+        if (direct) wt = exp2_of(sum_of(sSum[k & 1][u.c][u.h][L - 1]) - cs);
+        sWt[k & 1][u.c][u.h][u.i] = sStep[k & 1][u.c][u.h][u.i] * wt;
+        if (u.i == 0) {
+            sBase[k & 1][u.c][u.h] = after;
+            sScale[k & 1][u.c][u.h] = scale;
+            sDirect[k & 1][u.c][u.h] = direct;
+        }
+    };
+    float dt_next = 0.f;
+    if (nck > 0) {
+        offsets(L);
+        load(0);
+        if constexpr (OUT) {
+            if (tid < L * L / 8) *(f32x4 *)((char *)sM + tid * 8 * sizeof(ET)) = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (sizeof(ET) == 4 && tid < L * L / 8) *(f32x4 *)((char *)sM + tid * 32 + 16) = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        if (forms) {
+            steps(0, load_dt(0));
+            dt_next = load_dt(1);
         }
         __syncthreads();
+        if (forms) weights(0);
+        __syncthreads();
+    }
+    double total = 0.;          // sum of a over the segment
+    for (int c = 0; c < nck; ++c) {
+        const int k = (c / GC) & 1, cg = c % GC, rows = min(L, w.len - c * L);
+        ET *tB = sB[c & 1], *tC = sC[OUT ? c & 1 : 0], *tX = sX[c & 1], *tZ = sZ[GATED ? c & 1 : 0];
+        rB.store(tB, tid);
+        rX.store(tX, tid);
+        if constexpr (OUT) rC.store(tC, tc);
+        if constexpr (GATED) rZ.store(tZ, tid);
+        const float scale = sScale[k][cg][wh];
+        const bool direct = __builtin_amdgcn_readfirstlane(sDirect[k][cg][wh]);
+        if constexpr (!OUT) total += sum_of(sSum[k][cg][wh][L - 1]);
+        __syncthreads();
         if (c + 1 < nck) load(c + 1);
+        if (forms && cg == 0) {
+            steps(c / GC + 1, dt_next);
+            dt_next = load_dt(c / GC + 2);
+        }
+        if (forms && cg == 1) weights(c / GC + 1);
 
-        // x^T fragments: lane = column, elements = tokens
-        Frag8<ET> fx[2];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) col_frag<ET, 8>(fx[ks], tX, ks, 0, lane);
-
+        f32x4 Y[2] = {};
+        if (__builtin_amdgcn_readfirstlane(__float_as_int(scale)) != __float_as_int(1.f)) scale_state(scale);
         if constexpr (OUT) {
-            f32x16 G = {}, Y = {};
+            // the three 16 x 16 tiles of C B^T that hold j <= i, by three of the waves in turn
+            const int job = (wave - 3 * c) & (NW - 1);
+            if (job < 3) {
+                const int jt = job >> 1, it = (job + 1) >> 1;
+                f32x4 G = {};
 #pragma unroll
-            for (int ks = 0; ks < N / 16; ++ks) {
-                Frag8<ET> fb, fc, fs;
-                row_frag<ET, U>(fc, tC, l32, ks, g);
-                row_frag<ET, U>(fb, tB, l32, ks, g);
-                float t8[8];
+                for (int a = 0; a < NA; ++a) {
+                    Frag8<ET> fb, fc;
+                    fb.load8(tB + rn.at(jt, a));
+                    fc.load8(tC + rn.at(it, a));
+                    mma16(G, fb, fc);               // row j = 4 g + r, column i = l16
+                }
+                float m4[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t8[e] = S[ks >> 1][8 * (ks & 1) + e];
+                for (int r = 0; r < 4; ++r) m4[r] = (jt != it || 4 * g + r <= l16) ? G[r] : 0.f;
+                Vec4<ET>::store(sM + m_at(16 * it + l16, 4 * jt + g), Vec4<ET>::pack(m4));
+            }
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                Frag8<ET> fs, fc;
+                const float t8[8] = {S[2 * a][0], S[2 * a][1], S[2 * a][2], S[2 * a][3],
+                                     S[2 * a + 1][0], S[2 * a + 1][1], S[2 * a + 1][2], S[2 * a + 1][3]};
                 fs.set(t8);
-                mma32(G, fb, fc);           // (B C^T)[j][i]: column i = lane
-                mma32(Y, fs, fc);           // (S^T C^T)[p][i]
-            }
-            const float ei = __builtin_amdgcn_exp2f(ci);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) Y[e] *= ei;
-            float M[16];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 cj = *(const float4 *)&sAux[wave][0][8 * q + 4 * g];
-                const float4 sj = *(const float4 *)&sAux[wave][1][8 * q + 4 * g];
-                const float c4[4] = {cj.x, cj.y, cj.z, cj.w}, s4[4] = {sj.x, sj.y, sj.z, sj.w};
-                float d4[4] = {ci - c4[0], ci - c4[1], ci - c4[2], ci - c4[3]};
-                if constexpr (FINE) {
-                    const float4 lj = *(const float4 *)&sAux[wave][3][8 * q + 4 * g];
-                    d4[0] += cl - lj.x; d4[1] += cl - lj.y; d4[2] += cl - lj.z; d4[3] += cl - lj.w;
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float v = G[4 * q + r] * (__builtin_amdgcn_exp2f(d4[r]) * s4[r]);
-                    M[4 * q + r] = 8 * q + 4 * g + r <= l32 ? v : 0.f;
-                }
-            }
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                Frag8<ET> fm;
-                float t8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t8[e] = M[8 * ks + e];
-                fm.set(t8);
-                mma32(Y, fx[ks], fm);
-            }
-            // lane = token, registers = columns 8 q + 4 g + 0..3
-            if (live && l32 < rows) {
-                ET *dst = o + ((int64_t)c * L + l32) * p.o_st + 4 * g;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float x4[4], y4[4];
-                    Vec4<ET>::unpack(lds_unit<ET, 8>(tX, l32, 2 * q + g), x4);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y4[r] = __builtin_fmaf(skip, x4[r], Y[4 * q + r]);
-                    if (z) {
-                        float z4[4];
-                        Vec4<ET>::unpack(lds_unit<ET, 8>(tZ, l32, 2 * q + g), z4);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) y4[r] *= silu_act(z4[r]);
-                    }
-                    Vec4<ET>::store(dst + 8 * q, Vec4<ET>::pack(y4));
+                for (int it = 0; it < 2; ++it) {
+                    fc.load8(tC + rn.at(it, a));
+                    mma16(Y[it], fs, fc);           // (Z^T C^T)[p][i]
                 }
             }
         }
-        // state update
-        const float et = __builtin_amdgcn_exp2f(tot);
-        total2 += tot;
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) S[m][e] *= et;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const float4 wa = *(const float4 *)&sAux[wave][2][16 * ks + 4 * g];
-            const float4 wb = *(const float4 *)&sAux[wave][2][16 * ks + 8 + 4 * g];
+        // weighted x^T (lane = column, elements = tokens 4 g .. + 3 and 16 + 4 g .. + 3)
+        Frag8<ET> fx, fw[PARTS];
+        cx.get(fx, tX, 0, 0);
+        {
+            const float4 wa = *(const float4 *)&sWt[k][cg][wh][4 * g], wb = *(const float4 *)&sWt[k][cg][wh][16 + 4 * g];
             const float w8[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-            float xw[8];
-            if constexpr (sizeof(ET) == 2) {
-                const uint4 u = __builtin_bit_cast(uint4, fx[ks].v);
-                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+            if constexpr (BF) {
+                float xw[8];
+                const uint4 v = __builtin_bit_cast(uint4, fx.v);
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    xw[2 * e] = __builtin_bit_cast(float, uw[e] << 16) * w8[2 * e];
-                    xw[2 * e + 1] = __builtin_bit_cast(float, uw[e] & 0xffff0000u) * w8[2 * e + 1];
+                    xw[2 * e] = __builtin_bit_cast(float, vw[e] << 16) * w8[2 * e];
+                    xw[2 * e + 1] = __builtin_bit_cast(float, vw[e] & 0xffff0000u) * w8[2 * e + 1];
                 }
-                Frag8<bf16> part[3];
-                split3(xw, part);
-#pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    Frag8<bf16> fb;
-                    col_frag<bf16, U>(fb, tB, ks, m, lane);
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) mma32(S[m], fb, part[i]);
-                }
+                split3(xw, fw);
             } else {
-                Frag8<float> fw;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) fw.v[e] = fx[ks].v[e] * w8[e];
+                for (int e = 0; e < 8; ++e) fw[0].v[e] = fx.v[e] * w8[e];
+            }
+        }
+        if (direct) scale_state(exp2_of(sum_of(sSum[k][cg][wh][L - 1])));
+        // state update: neighbouring products belong to different tiles
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    Frag8<float> fb;
-                    col_frag<float, U>(fb, tB, ks, m, lane);
-                    mma32(S[m], fb, fw);
+        for (int a = 0; a < NA; ++a) {
+            Frag8<ET> fb[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) cn.get(fb[t], tB, a, t);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) mma16(S[2 * a + t], fb[t], fw[i]);
+        }
+        if constexpr (OUT) {
+            __syncthreads();                        // sM
+            const float ei[2] = {sEi[k][cg][wh][l16], sEi[k][cg][wh][16 + l16]};
+            if (!direct) {
+                Frag8<ET> fm[2];
+#pragma unroll
+                for (int it = 0; it < 2; ++it) fm[it].load44(sM + m_at(16 * it + l16, g), sM + m_at(16 * it + l16, 4 + g));
+#pragma unroll
+                for (int i = 0; i < (BF ? 2 : 1); ++i)
+#pragma unroll
+                    for (int it = 0; it < 2; ++it) mma16(Y[it], fw[i], fm[it]);
+#pragma unroll
+                for (int it = 0; it < 2; ++it)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) Y[it][r] *= ei[it];
+            } else {
+                // every weight a difference of sums: step_j e^{c_i - c_j} on M, plain x.  (The
+                // addresses are formed here: held through the loop they would cost its registers.)
+                const int hl = here(lane), hi = hl & 15, hg = hl >> 4;
+#pragma unroll
+                for (int it = 0; it < 2; ++it) {
+                    const float2 ci = sSum[k][cg][wh][16 * it + hi];
+                    float m8[8];
+                    Frag8<ET> fd, fp;
+                    fd.load44(sM + m_at(16 * it + hi, hg), sM + m_at(16 * it + hi, 4 + hg));
+                    if constexpr (BF) {
+                        const uint4 v = __builtin_bit_cast(uint4, fd.v);
+                        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            m8[2 * e] = __builtin_bit_cast(float, vw[e] << 16);
+                            m8[2 * e + 1] = __builtin_bit_cast(float, vw[e] & 0xffff0000u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) m8[e] = fd.v[e];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int j = 16 * (q >> 1) + 4 * hg + 2 * (q & 1);
+                        const float2 sj = *(const float2 *)&sStep[k][cg][wh][j];
+                        const float4 cj = *(const float4 *)&sSum[k][cg][wh][j];
+                        m8[2 * q] *= sj.x * __builtin_amdgcn_exp2f(fminf((ci.x - cj.x) + (ci.y - cj.y), 0.f));
+                        m8[2 * q + 1] *= sj.y * __builtin_amdgcn_exp2f(fminf((ci.x - cj.z) + (ci.y - cj.w), 0.f));
+                    }
+                    fd.set(m8);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) Y[it][r] *= ei[it];
+                    Cols<ET, XC, false>(hl, wh * P + slab * 16).get(fp, tX, 0, 0);
+                    mma16(Y[it], fp, fd);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+            }
+            // lane = token, registers = columns 4 g .. + 3 of the slab
+            ET *dst = (ET *)p.o + seq * p.o_sb + (w.tok + (int64_t)c * L) * p.o_st + h * p.o_sh + slab * 16 + 4 * g;
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                float x4[4], y4[4];
+                Vec4<ET>::unpack(Vec4<ET>::load(tX + xrow + it * 16 * XC), x4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y4[r] = __builtin_fmaf(skip, x4[r], Y[it][r]);
+                if constexpr (GATED) {
+                    float z4[4];
+                    Vec4<ET>::unpack(Vec4<ET>::load(tZ + xrow + it * 16 * XC), z4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y4[r] *= silu_act(z4[r]);
+                }
+                if (live && 16 * it + l16 < rows) Vec4<ET>::store(dst + (uint32_t)(16 * it + l16) * (uint32_t)p.o_st, Vec4<ET>::pack(y4));
             }
         }
     }
+    if (nck > 0) {
+        const double b = sBase[((nck - 1) / GC) & 1][(nck - 1) % GC][wh];
+        if (b != 0.) scale_state(exp2_of(b));
+    }
+    if (!live) return;
     if constexpr (!OUT) {
-        if (!live) return;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) *(f32x4 *)(ws + ws_index<P, N>(slab, m, lane)) = S[m];
+        if (slab == 0 && lane == 0) p.ws_decay[(int64_t)slot * p.H + h] = total;
+    } else if (w.last && p.sT) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *(float4 *)(ws + ws_index<P, N>(slab, m, q, lane)) =
-                    make_float4(S[m][4 * q], S[m][4 * q + 1], S[m][4 * q + 2], S[m][4 * q + 3]);
-        if (slab == 0 && lane == 0) p.ws_decay[(int64_t)slot * p.H + h] = total2;
-    } else if (live && w.last && p.sT) {
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = 32 * m + 8 * (e >> 2) + 4 * g + (e & 3);
-                const int64_t i = w.n * p.sT_sn + h * p.sT_sh + row * p.sT_sr + slab * 32 + l32;
-                if (p.sT_bf16) ((bf16 *)p.sT)[i] = (bf16)S[m][e];
-                else ((float *)p.sT)[i] = S[m][e];
+            for (int r = 0; r < 4; ++r) {
+                const int64_t i = w.n * p.sT_sn + h * p.sT_sh + row_of(m, g, r) * p.sT_sr + slab * 16 + l16;
+                if (p.sT_bf16) ((bf16 *)p.sT)[i] = (bf16)S[m][r];
+                else ((float *)p.sT)[i] = S[m][r];
             }
     }
 }
@@ -464,8 +650,8 @@ __global__ __launch_bounds__(256) void ssm_scan_kernel(const SsmParams p)
     const int part = blockIdx.x % BPS;
     const int64_t chain = blockIdx.x / BPS;
     const int n = (int)(chain / p.H), h = (int)(chain % p.H);
-    const int i4 = part * 256 + threadIdx.x, lane = i4 & 63, g = lane >> 5;
-    const int q = (i4 >> 6) & 3, m = (i4 >> 8) % (N / 32), slab = i4 / (64 * 4 * (N / 32));
+    const int i4 = part * 256 + threadIdx.x, lane = i4 & 63;
+    const int m = (i4 >> 6) % (N / 16), slab = i4 / (64 * (N / 16));
     int slot, count;
     if (p.cu) {
         slot = p.cu[n] / p.seg + n;
@@ -477,15 +663,15 @@ __global__ __launch_bounds__(256) void ssm_scan_kernel(const SsmParams p)
     float s[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        s[r] = p.s0 ? ld_any(p.s0, n * p.s0_sn + h * p.s0_sh + (32 * m + 8 * q + 4 * g + r) * p.s0_sr + slab * 32 + (lane & 31),
+        s[r] = p.s0 ? ld_any(p.s0, n * p.s0_sn + h * p.s0_sh + row_of(m, lane >> 4, r) * p.s0_sr + slab * 16 + (lane & 15),
                              p.s0_bf16)
                     : 0.f;
     float *ws = p.ws_state + ((int64_t)slot * p.H + h) * (N * P) + i4 * 4;
-    const float *dec = p.ws_decay + (int64_t)slot * p.H + h;
+    const double *dec = p.ws_decay + (int64_t)slot * p.H + h;
     const int64_t step = (int64_t)p.H * (N * P);
     for (int k = 0; k + 1 < count; ++k) {
         const float4 e = *(const float4 *)ws;
-        const float d = __builtin_amdgcn_exp2f(*dec);
+        const float d = exp2_of(*dec);
         *(float4 *)ws = make_float4(s[0], s[1], s[2], s[3]);
         s[0] = __builtin_fmaf(s[0], d, e.x);
         s[1] = __builtin_fmaf(s[1], d, e.y);
@@ -502,10 +688,10 @@ static hipError_t launch_t(const SsmParams &p, bool states_only, hipStream_t st)
 {
     const int64_t blocks = (int64_t)p.slots * p.wg_per_slot;
     if (blocks <= 0) return hipSuccess;
-    if (states_only)
-        hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, false>), dim3((unsigned)blocks), dim3(HPW * P * 2), 0, st, p);
-    else
-        hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true>), dim3((unsigned)blocks), dim3(HPW * P * 2), 0, st, p);
+    const dim3 grid((unsigned)blocks), thr(HPW * P * 4);
+    if (states_only) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, false, false>), grid, thr, 0, st, p);
+    else if (p.z) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, false>), grid, thr, 0, st, p);
     return hipGetLastError();
 }
 
