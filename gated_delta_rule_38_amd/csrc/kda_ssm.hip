@@ -573,6 +573,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                     float m8[8];
                     Frag8<ET> fd, fp;
                     fd.load44(sM + m_at(16 * it + hi, hg), sM + m_at(16 * it + hi, 4 + hg));
+                    __builtin_amdgcn_sched_barrier(0);
                     if constexpr (BF) {
                         const uint4 v = __builtin_bit_cast(uint4, fd.v);
                         const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
@@ -592,6 +593,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                         const float4 cj = *(const float4 *)&sSum[k][cg][wh][j];
                         m8[2 * q] *= sj.x * __builtin_amdgcn_exp2f(fminf((ci.x - cj.x) + (ci.y - cj.y), 0.f));
                         m8[2 * q + 1] *= sj.y * __builtin_amdgcn_exp2f(fminf((ci.x - cj.z) + (ci.y - cj.w), 0.f));
+                        __builtin_amdgcn_sched_barrier(0);      // (few registers at a time)
                     }
                     fd.set(m8);
 #pragma unroll
