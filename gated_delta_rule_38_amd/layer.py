@@ -1,31 +1,25 @@
 """The operators around the recurrence (C ABI in ``include/kda_layer.h``): the short causal
 convolution, the query/key norm with rotation and the selective state space scan.
 
-Marshalling only, like the rest of the package, and kept short: these calls run in single-token
-steps whose kernels take a few microseconds, so descriptors are packed into one buffer per call.
-Every call runs with the device of its first tensor current, on that device's current stream unless
-one is given; outputs and workspaces it allocates are allocated on that stream.
+Marshalling only, like the rest of the package: a small extension module (``csrc/layer_binding.cpp``)
+describes the tensors, allocates what was not given and calls the library.  Every call runs with the
+device of its first tensor current, on that device's current stream unless one is given; outputs and
+workspaces it allocates are allocated on that stream.
 """
 from __future__ import annotations
 
 import ctypes
 import math
-import struct
 from typing import Optional, Tuple
 
-_DESC = struct.Struct("<Qii4q4q")          # kda_tensor_t
-_SIZE = _DESC.size
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
-_SSM_OPTS = struct.Struct("<QQQii")        # kda_ssm_options_t
-_QK_OPTS = struct.Struct("<ifiif")         # kda_qk_norm_options_t
-_codes = None
 _activations = {None: 0, "none": 0, "silu": 1}
 _norms = {None: 0, "none": 0, "rms": 1, "l2": 2}
 _layouts = {"half": 0, "interleaved": 1}
+_ext = None
 
 
 def bind(lib) -> None:
-    """Argument types of the functions (descriptor addresses are plain integers)."""
+    """Argument types of the functions for callers of the C ABI (descriptor addresses as integers)."""
     V, I = ctypes.c_void_p, ctypes.c_int32
     for name, args in (("kda_conv", [V] * 7 + [I, V]), ("kda_conv_decode", [V] * 7 + [I, I, V]),
                        ("kda_qk_norm", [V] * 10), ("kda_ssm_prefill", [V] * 11),
@@ -37,87 +31,33 @@ def bind(lib) -> None:
         fn.restype = ctypes.c_int
 
 
-class _Call:
-    """The descriptors of one call's tensors, packed, and where it runs."""
-    __slots__ = ("buf", "ptr", "lib", "device", "stream", "guard")
-
-    def __init__(self, tensors, stream, extra=0):
-        import torch
-
-        from . import load_library
-        global _codes
-        if _codes is None:
-            _codes = {torch.bfloat16: 0, torch.float32: 1, torch.int32: 2}
-        self.lib = load_library()
-        device = tensors[0].device
-        if not torch.cuda.is_available():
-            raise RuntimeError("gated_delta_rule_38_amd needs a ROCm GPU (gfx950); none is visible")
-        self.buf = buf = ctypes.create_string_buffer(_SIZE * len(tensors) + extra)
-        base = ctypes.addressof(buf)
-        self.ptr = ptr = []
-        at = 0
-        for t in tensors:
-            if t is None:
-                ptr.append(None)
-            else:
-                if t.device != device or not t.is_cuda:
-                    raise ValueError("all tensors must be on one GPU")
-                shape = t.shape
-                n = len(shape)
-                if n > 4:
-                    raise ValueError("at most 4 dimensions")
-                pad = _PAD[n]
-                _DESC.pack_into(buf, at, t.data_ptr(), _codes.get(t.dtype, -1), n, *shape, *pad, *t.stride(), *pad)
-                ptr.append(base + at)
-            at += _SIZE
-        self.device = device
-        self.stream, self.guard = _where(device, stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def check(self, status):
-        if status:
-            from . import KdaError
-            raise KdaError(status, self.lib.kda_last_error().decode())
-
-
-def _where(device, stream):
-    """(raw stream, guard): the stream of a call, and the context that makes its device and stream
-    current while it runs (None when they already are)."""
+def _binding():
+    """The extension module, attached to the loaded library."""
+    global _ext
     import torch
-    index = device.index
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
-        if torch.cuda.current_device() == index:
-            return raw, None
-        return raw, torch.cuda.device(device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+
+    from . import KdaError, load_library
+    if not torch.cuda.is_available():
+        raise RuntimeError("gated_delta_rule_38_amd needs a ROCm GPU (gfx950); none is visible")
+    lib = load_library()
+    try:
+        from . import _layer_binding as ext
+    except ImportError as e:
+        raise ImportError(f"{e}: build it with `python -m gated_delta_rule_38_amd.build`") from e
+    ext.attach(KdaError, torch._C._cuda_getCurrentRawStream,
+               *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                 for name in ("kda_conv", "kda_conv_decode", "kda_qk_norm", "kda_ssm_workspace_size",
+                              "kda_ssm_prefill_ws", "kda_ssm_decode", "kda_last_error")))
+    _ext = ext
+    return ext
 
 
-def _empty_like(t, device, stream):
-    """A contiguous tensor of t's shape and dtype, allocated on the call's stream."""
-    return _empty(t.shape, t.dtype, device, stream)
-
-
-def _empty(shape, dtype, device, stream):
+def _on(stream, x):
+    """The context that makes ``stream`` (a torch.cuda.Stream or a raw handle) current."""
     import torch
-    if not device.type == "cuda":
-        raise ValueError("all tensors must be on one GPU")
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    return torch.cuda.stream(stream)
 
 
 def _lookup(table, key, what):
@@ -137,16 +77,12 @@ def conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, out=None, fi
     first; ``final_state`` may be ``initial_state`` itself.  A final state allocated here has
     ``initial_state``'s dtype, or x's.
     """
-    act = _lookup(_activations, activation, "activation")
-    if out is None:
-        out = _empty_like(x, x.device, stream)
-    if final_state is None and output_final_state:
-        n = cu_seqlens.numel() - 1 if cu_seqlens is not None else x.shape[0]
-        dtype = initial_state.dtype if initial_state is not None else x.dtype
-        final_state = _empty((n, weight.shape[-1] - 1, x.shape[-1]), dtype, x.device, stream)
-    with _Call((x, weight, bias, initial_state, cu_seqlens, out, final_state), stream) as c:
-        c.check(c.lib.kda_conv(*c.ptr, act, c.stream))
-    return out, final_state
+    args = (x, weight, bias, initial_state, cu_seqlens, out, final_state, output_final_state,
+            _lookup(_activations, activation, "activation"))
+    if stream is not None:
+        with _on(stream, x):
+            return (_ext or _binding()).conv(*args)
+    return (_ext or _binding()).conv(*args)
 
 
 def conv_decode(x, weight, state_pool, state_indices, num_tokens=None, bias=None, out=None,
@@ -157,12 +93,12 @@ def conv_decode(x, weight, state_pool, state_indices, num_tokens=None, bias=None
     the GPU, with ``decode``'s meaning (a slot outside [0, P) skips the request).
     ``update_state=False`` only reads the pool (verify); ``write_out=False`` only commits.
     """
-    act = _lookup(_activations, activation, "activation")
-    if out is None and write_out:
-        out = _empty_like(x, x.device, stream)
-    with _Call((x, weight, bias, state_pool, state_indices, num_tokens, out), stream) as c:
-        c.check(c.lib.kda_conv_decode(*c.ptr, int(update_state), act, c.stream))
-    return out
+    args = (x, weight, bias, state_pool, state_indices, num_tokens, out, write_out, update_state,
+            _lookup(_activations, activation, "activation"))
+    if stream is not None:
+        with _on(stream, x):
+            return (_ext or _binding()).conv_decode(*args)
+    return (_ext or _binding()).conv_decode(*args)
 
 
 def qk_norm(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq=None, norm: Optional[str] = "rms",
@@ -178,17 +114,14 @@ def qk_norm(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq=No
     "interleaved": neighbours), cos and sin times ``rotary_scale``; without them nothing rotates.
     ``q_out=q`` and ``k_out=k`` work in place, also on slices of one fused projection.
     """
-    opts = (_lookup(_norms, norm, "norm"), eps, _lookup(_layouts, layout, "layout"), rotary_offset, rotary_scale)
     if inv_freq is not None and inv_freq.numel() == 0:
         inv_freq = None
-    if q_out is None:
-        q_out = _empty_like(q, q.device, stream)
-    if k_out is None and k is not None:
-        k_out = _empty_like(k, q.device, stream)
-    with _Call((q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out), stream, _QK_OPTS.size) as c:
-        _QK_OPTS.pack_into(c.buf, 8 * _SIZE, *opts)
-        c.check(c.lib.kda_qk_norm(*c.ptr, ctypes.addressof(c.buf) + 8 * _SIZE, c.stream))
-    return q_out, k_out
+    args = (q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, _lookup(_norms, norm, "norm"), eps,
+            _lookup(_layouts, layout, "layout"), rotary_offset, rotary_scale)
+    if stream is not None:
+        with _on(stream, q):
+            return (_ext or _binding()).qk_norm(*args)
+    return (_ext or _binding()).qk_norm(*args)
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
@@ -233,11 +166,6 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] =
     return inv.float().to(device), scale
 
 
-def _ssm_opts(c, at, ptrs, softplus, segment=0):
-    _SSM_OPTS.pack_into(c.buf, at, *(p or 0 for p in ptrs), int(bool(softplus)), segment)
-    return ctypes.addressof(c.buf) + at
-
-
 def ssm_prefill(x, dt, A, B, C, D=None, dt_bias=None, z=None, initial_state=None, cu_seqlens=None, out=None,
                 final_state=None, output_final_state: bool = True, dt_softplus: bool = False, segment: int = 0,
                 workspace=None, stream=None) -> Tuple:
@@ -250,40 +178,17 @@ def ssm_prefill(x, dt, A, B, C, D=None, dt_bias=None, z=None, initial_state=None
     States [N_seq, H, N, P]; a final state allocated here is fp32.  ``workspace``: an optional uint8
     tensor of at least ``ssm_workspace_size`` + 256 bytes; by default torch allocates one.
     """
-    if out is None:
-        out = _empty_like(x, x.device, stream)
-    if final_state is None and output_final_state:
-        import torch
-        n = cu_seqlens.numel() - 1 if cu_seqlens is not None else x.shape[0]
-        final_state = _empty((n, x.shape[-2], B.shape[-1], x.shape[-1]), torch.float32, x.device, stream)
-    with _Call((x, dt, A, B, C, initial_state, cu_seqlens, out, final_state, D, dt_bias, z), stream,
-               _SSM_OPTS.size + 8) as c:
-        opts = _ssm_opts(c, 12 * _SIZE, c.ptr[9:], dt_softplus, segment)
-        need = ctypes.c_size_t.from_buffer(c.buf, 12 * _SIZE + _SSM_OPTS.size)
-        c.check(c.lib.kda_ssm_workspace_size(*c.ptr[:9], opts, ctypes.addressof(need)))
-        base = size = 0
-        if need.value:
-            if workspace is None:
-                import torch
-                workspace = _empty((need.value + 256,), torch.uint8, x.device, stream)
-            elif workspace.device != x.device or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on the operands' GPU")
-            start = workspace.data_ptr()
-            base = (start + 255) // 256 * 256
-            size = max(0, workspace.numel() * workspace.element_size() - (base - start))
-        c.check(c.lib.kda_ssm_prefill_ws(*c.ptr[:9], opts, base, size, c.stream))
-    return out, final_state
+    args = (x, dt, A, B, C, initial_state, cu_seqlens, out, final_state, D, dt_bias, z, workspace, output_final_state,
+            dt_softplus, segment)
+    if stream is not None:
+        with _on(stream, x):
+            return (_ext or _binding()).ssm_prefill(*args)
+    return (_ext or _binding()).ssm_prefill(*args)
 
 
 def ssm_workspace_size(x, dt, A, B, C, initial_state=None, cu_seqlens=None, segment: int = 0) -> int:
     """Bytes of workspace ``ssm_prefill`` needs for these tensors."""
-    import torch
-    out = torch.empty_like(x)
-    with _Call((x, dt, A, B, C, initial_state, cu_seqlens, out, None), None, _SSM_OPTS.size + 8) as c:
-        opts = _ssm_opts(c, 9 * _SIZE, (0, 0, 0), False, segment)
-        need = ctypes.c_size_t.from_buffer(c.buf, 9 * _SIZE + _SSM_OPTS.size)
-        c.check(c.lib.kda_ssm_workspace_size(*c.ptr, opts, ctypes.addressof(need)))
-        return need.value
+    return (_ext or _binding()).ssm_workspace_size(x, dt, A, B, C, initial_state, cu_seqlens, segment)
 
 
 def ssm_decode(x, dt, A, B, C, state_pool, state_indices, num_tokens=None, D=None, dt_bias=None, z=None, out=None,
@@ -294,10 +199,9 @@ def ssm_decode(x, dt, A, B, C, state_pool, state_indices, num_tokens=None, D=Non
     ``num_tokens`` int32 [R] on the GPU with ``decode``'s meaning; ``update_state=False`` only reads
     the pool (verify), ``write_out=False`` only commits.
     """
-    if out is None and write_out:
-        out = _empty_like(x, x.device, stream)
-    with _Call((x, dt, A, B, C, state_pool, state_indices, num_tokens, out, D, dt_bias, z), stream,
-               _SSM_OPTS.size) as c:
-        opts = _ssm_opts(c, 12 * _SIZE, c.ptr[9:], dt_softplus)
-        c.check(c.lib.kda_ssm_decode(*c.ptr[:9], int(update_state), opts, c.stream))
-    return out
+    args = (x, dt, A, B, C, state_pool, state_indices, num_tokens, out, D, dt_bias, z, write_out, update_state,
+            dt_softplus)
+    if stream is not None:
+        with _on(stream, x):
+            return (_ext or _binding()).ssm_decode(*args)
+    return (_ext or _binding()).ssm_decode(*args)

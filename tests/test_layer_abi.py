@@ -319,10 +319,10 @@ def test_layer_binding_refuses_without_gpu():
     if torch.cuda.is_available():
         pytest.skip("a GPU is visible")
     x, w = torch.zeros(4, 64), torch.zeros(64, 4)
-    with pytest.raises(ValueError):
+    with pytest.raises(RuntimeError):
         kda.conv(x, w)
     with pytest.raises(RuntimeError):
-        kda.conv(x, w, out=x, output_final_state=False)
+        kda.ssm_workspace_size(x, x, x, x, x)
     with pytest.raises(ValueError):
         kda.conv(x, w, activation="relu")
     with pytest.raises(ValueError):
