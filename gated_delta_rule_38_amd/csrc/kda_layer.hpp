@@ -143,7 +143,7 @@ struct SsmParams {
     int32_t heads_per_wg;
     int32_t wide;              // x, z, B, C rows are 16-byte aligned (else 8-byte, bf16)
     float *ws_state;           // [slots][H][N x P]
-    double *ws_decay;          // [slots][H]: sum of A step over the segment, in powers of two
+    float *ws_decay;           // [slots][H]: e to the sum of A step over the segment
 };
 // states_only: the end state of every segment from a zero start, and its decay (pass 1);
 // otherwise the outputs.

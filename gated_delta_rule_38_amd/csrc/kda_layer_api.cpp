@@ -506,29 +506,60 @@ kda_status_t ssm_state(const kda_tensor_t *t, const char *name, int64_t n, int64
     return KDA_OK;
 }
 
-// Segment length of a batch: whole sequences when their workgroups fill the chip, else the tokens
-// of all sequences cut evenly over about two workgroups a CU.
-void ssm_plan(Ssm &s, const kda_ssm_options_t *o)
+// Microseconds of one pass over `chunks` chunks by `workgroups` workgroups: `alone` a chunk while every
+// workgroup has its CU to itself, towards `shared` as two sit on some CUs (the pass ends with those)
+// and on all (512 at once), rounds beyond that; one is the most a CU holds of the fp32 kernel.
+double ssm_pass(double workgroups, double chunks, double alone, double shared, bool f32)
+{
+    if (workgroups <= 256) return chunks * alone;
+    if (f32) return chunks * alone * workgroups / 256;
+    if (workgroups <= 512) return chunks * (alone + (shared - alone) * (0.5 + 0.5 * (workgroups - 256) / 256));
+    return chunks * shared * workgroups / 512;
+}
+
+// Segment length of a batch (0: whole sequences), by a cost in microseconds fitted to MI355X.  Whole
+// sequences: one pass.  Segments: the states' pass (1.4 us a chunk, shared or not), the outputs' pass
+// (2.3 alone, 4.3 shared, 3.7 with 64 state channels), the states' way through memory (written, turned
+// into start states, read: 2.35 TB/s) and the scan's walk; 2.4 times as much a chunk in fp32.  The
+// lengths of a packed batch are on the device: a whole run is charged a longest sequence of 1.7 times
+// the mean, whose end it runs alone, and segments half a segment of waste a sequence.
+// On 15 batches of 203 to 65,536 tokens and 4 to 64 heads, against 5 to 16 forced lengths each, the
+// choice is within 7% of the best but for one packed batch (16% and more where its few lengths fit a
+// round of workgroups exactly, which the host cannot see).
+void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32)
 {
     const int64_t hg = s.H / s.G;
     s.hpw = s.P == 64 && hg > 1 ? 2 : 1;
     s.wps = s.G * ((hg + s.hpw - 1) / s.hpw);
-    const int64_t longest = s.L.dense ? s.L.T : s.L.tokens;    // the longest a sequence can be
-    const int64_t cus = device_cus();
+    const int64_t N = s.L.N, longest = s.L.dense ? s.L.T : s.L.tokens;    // the longest a sequence can be
     const int asked = o ? o->segment : 0;
-    if (asked > 0) s.seg = asked;
-    else if (asked < 0 || s.L.N * s.wps >= 2 * cus) s.seg = 0;
-    else {
-        s.seg = std::max<int64_t>(128, (s.L.tokens * s.wps / (2 * cus) + 31) / 32 * 32);
+    s.seg = std::max(0, asked);
+    if (asked == 0 && N > 0 && longest > kda::SSM_CHUNK) {
+        const double cl = kda::SSM_CHUNK, per = f32 ? 2.4 : 1., shared = s.N == 64 ? 3.7 : 4.3;
+        const double half = s.P == 64 && s.hpw == 1 ? 0.5 : 1.;     // (workgroups of half the size)
+        const double T = (double)s.L.tokens, n = (double)N, wgs = (double)s.wps * half;
+        const double likely = s.L.dense || N == 1 ? (double)longest : std::min((double)longest, 1.7 * T / n);
+        const double mean = std::ceil(T / n / cl);
+        double best = per * (ssm_pass(n * wgs, mean, 2.3, shared, f32) + (std::ceil(likely / cl) - mean) * 2.3);
+        for (int64_t seg = 32; seg < longest && seg <= 8192; seg += seg < 256 ? 32 : seg < 1024 ? 128 : 256) {
+            const double segs = s.L.dense || N == 1 ? n * std::ceil((double)longest / (double)seg) : T / (double)seg + 0.5 * n;
+            const double chunks = (double)seg / cl, states = std::max(0., segs - n) * (double)s.H * (double)(s.N * s.P) * 8.;
+            const double cost = per * (ssm_pass((segs - n) * wgs, chunks, 1.4, 1.4, f32) + ssm_pass(segs * wgs, chunks, 2.3, shared, f32)) +
+                                states / 2.35e6 + 0.03 * likely / (double)seg;
+            if (cost < best) {
+                best = cost;
+                s.seg = seg;
+            }
+        }
     }
     if (s.seg >= longest) s.seg = 0;
     if (s.seg == 0) {
-        s.slots = s.L.N;
+        s.slots = N;
         return;
     }
-    s.slots = s.L.dense ? s.L.N * std::max<int64_t>(1, (s.L.T + s.seg - 1) / s.seg) : s.L.tokens / s.seg + s.L.N;
+    s.slots = s.L.dense ? N * std::max<int64_t>(1, (s.L.T + s.seg - 1) / s.seg) : s.L.tokens / s.seg + N;
     s.off_decay = align256((size_t)s.slots * s.H * s.N * s.P * 4);
-    s.bytes = s.off_decay + align256((size_t)s.slots * s.H * 8);
+    s.bytes = s.off_decay + align256((size_t)s.slots * s.H * 4);
 }
 
 kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_tensor_t *A, const kda_tensor_t *B,
@@ -584,7 +615,7 @@ kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_
     if (sT && overlaps(span_of(sT), span_of(out))) return fail(KDA_ERR_ALIAS, "final_state overlaps out");
     KDA_TRY(distinct_rows(out, "out"));
     KDA_TRY(distinct_rows(sT, "final_state"));
-    ssm_plan(s, o);
+    ssm_plan(s, o, x->dtype == KDA_F32);
     if (s.slots * s.wps > (int64_t)INT32_MAX || s.L.N * s.H * (s.N * s.P / 1024) > (int64_t)INT32_MAX)
         return fail(KDA_ERR_UNSUPPORTED, "too many workgroups for one launch");
     if (env_on("KDA_LOG"))
@@ -619,7 +650,7 @@ kda_status_t ssm_run(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_te
     p.seg = (int32_t)s.seg; p.slots = (int32_t)s.slots; p.wg_per_slot = (int32_t)s.wps; p.heads_per_wg = s.hpw;
     p.wide = aligned_to(x, 8) && aligned_to(B, 8) && aligned_to(C, 8) && aligned_to(s.tz, 8) && aligned_to(out, 8);
     p.ws_state = (float *)ws;
-    p.ws_decay = ws ? (double *)((char *)ws + s.off_decay) : nullptr;
+    p.ws_decay = ws ? (float *)((char *)ws + s.off_decay) : nullptr;
     const bool f32 = x->dtype == KDA_F32;
     hipError_t e;
     if (s.seg) {

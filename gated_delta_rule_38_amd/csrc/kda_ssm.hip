@@ -311,6 +311,8 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
     __shared__ double sBase[2][GC][HPW];
     __shared__ float sScale[2][GC][HPW];
     __shared__ int sDirect[2][GC][HPW];
+    __shared__ double sA[HPW];                          // A log2 e
+    __shared__ float sBias[HPW];
 
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -401,15 +403,14 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
         const Unit u = unit();
         const int t = min((k * GC + u.c) * L + u.i, w.len - 1);
         const int64_t at = seq * p.dt_sb + (w.tok + t) * p.dt_st + (h0 + min(u.h, heads - 1)) * p.dt_sh;
-        return k * GC < nck ? ld_any(p.dt, at, p.dt_bf16) : 0.f;
+        return forms && k * GC < nck ? ld_any(p.dt, at, p.dt_bf16) : 0.f;
     };
     auto steps = [&](int k, float raw) {            // tokens past the end: step 0
         const Unit u = unit();
-        const int hu = h0 + min(u.h, heads - 1);
-        const float step = (k * GC + u.c) * L + u.i < w.len ? step_of(raw + (p.dt_bias ? p.dt_bias[hu] : 0.f), p.softplus) : 0.f;
+        const float step = (k * GC + u.c) * L + u.i < w.len ? step_of(raw + sBias[u.h], p.softplus) : 0.f;
         sStep[k & 1][u.c][u.h][u.i] = step;
         // decays in powers of two; sums in 64 bits, kept as two floats
-        const double cs = prefix32((double)step * ((double)p.A[hu] * 1.4426950408889634));
+        const double cs = prefix32((double)step * sA[u.h]);
         sSum[k & 1][u.c][u.h][u.i] = make_float2((float)cs, (float)(cs - (double)(float)cs));
     };
     auto sum_of = [&](float2 v) { return (double)v.x + (double)v.y; };
@@ -455,10 +456,15 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
             if (tid < L * L / 8) *(f32x4 *)((char *)sM + tid * 8 * sizeof(ET)) = f32x4{0.f, 0.f, 0.f, 0.f};
             if (sizeof(ET) == 4 && tid < L * L / 8) *(f32x4 *)((char *)sM + tid * 32 + 16) = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        if (forms) {
-            steps(0, load_dt(0));
-            dt_next = load_dt(1);
+        const float dt0 = load_dt(0);
+        dt_next = load_dt(1);
+        if (tid < HPW) {
+            const int hu = h0 + min(tid, heads - 1);
+            sA[tid] = (double)p.A[hu] * 1.4426950408889634;
+            sBias[tid] = p.dt_bias ? p.dt_bias[hu] : 0.f;
         }
+        __syncthreads();
+        if (forms) steps(0, dt0);
         __syncthreads();
         if (forms) weights(0);
         __syncthreads();
@@ -550,7 +556,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
         }
         if constexpr (OUT) {
             __syncthreads();                        // sM
-            const float ei[2] = {sEi[k][cg][wh][l16], sEi[k][cg][wh][16 + l16]};
+            float ei[2] = {sEi[k][cg][wh][l16], sEi[k][cg][wh][16 + l16]};
             if (!direct) {
                 Frag8<ET> fm[2];
 #pragma unroll
@@ -559,10 +565,6 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                 for (int i = 0; i < (BF ? 2 : 1); ++i)
 #pragma unroll
                     for (int it = 0; it < 2; ++it) mma16(Y[it], fw[i], fm[it]);
-#pragma unroll
-                for (int it = 0; it < 2; ++it)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) Y[it][r] *= ei[it];
             } else {
                 // every weight a difference of sums: step_j e^{c_i - c_j} on M, plain x.  (The
                 // addresses are formed here: held through the loop they would cost its registers.)
@@ -600,6 +602,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                     for (int r = 0; r < 4; ++r) Y[it][r] *= ei[it];
                     Cols<ET, XC, false>(hl, wh * P + slab * 16).get(fp, tX, 0, 0);
                     mma16(Y[it], fp, fd);
+                    ei[it] = 1.f;
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -610,7 +613,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                 float x4[4], y4[4];
                 Vec4<ET>::unpack(Vec4<ET>::load(tX + xrow + it * 16 * XC), x4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) y4[r] = __builtin_fmaf(skip, x4[r], Y[it][r]);
+                for (int r = 0; r < 4; ++r) y4[r] = __builtin_fmaf(Y[it][r], ei[it], skip * x4[r]);
                 if constexpr (GATED) {
                     float z4[4];
                     Vec4<ET>::unpack(Vec4<ET>::load(tZ + xrow + it * 16 * XC), z4);
@@ -629,7 +632,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
     if constexpr (!OUT) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) *(f32x4 *)(ws + ws_index<P, N>(slab, m, lane)) = S[m];
-        if (slab == 0 && lane == 0) p.ws_decay[(int64_t)slot * p.H + h] = total;
+        if (slab == 0 && lane == 0) p.ws_decay[(int64_t)slot * p.H + h] = exp2_of(total);
     } else if (w.last && p.sT) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -669,20 +672,30 @@ __global__ __launch_bounds__(256) void ssm_scan_kernel(const SsmParams p)
                              p.s0_bf16)
                     : 0.f;
     float *ws = p.ws_state + ((int64_t)slot * p.H + h) * (N * P) + i4 * 4;
-    const double *dec = p.ws_decay + (int64_t)slot * p.H + h;
+    const float *dec = p.ws_decay + (int64_t)slot * p.H + h;
     const int64_t step = (int64_t)p.H * (N * P);
-    for (int k = 0; k + 1 < count; ++k) {
-        const float4 e = *(const float4 *)ws;
-        const float d = exp2_of(*dec);
-        *(float4 *)ws = make_float4(s[0], s[1], s[2], s[3]);
-        s[0] = __builtin_fmaf(s[0], d, e.x);
-        s[1] = __builtin_fmaf(s[1], d, e.y);
-        s[2] = __builtin_fmaf(s[2], d, e.z);
-        s[3] = __builtin_fmaf(s[3], d, e.w);
-        ws += step;
-        dec += p.H;
+    // the end states of AHEAD segments are requested before the first of them is needed: the walk
+    // itself is four FMAs a segment
+    constexpr int AHEAD = 16;
+    for (int k = 0; k < count; k += AHEAD) {
+        float4 e[AHEAD];
+        float d[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int64_t at = min(k + u, count - 2);       // the last one's end state is never read
+            e[u] = count > 1 ? *(const float4 *)(ws + at * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+            d[u] = count > 1 ? dec[at * p.H] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (k + u >= count) break;
+            *(float4 *)(ws + (k + u) * step) = make_float4(s[0], s[1], s[2], s[3]);
+            s[0] = __builtin_fmaf(s[0], d[u], e[u].x);
+            s[1] = __builtin_fmaf(s[1], d[u], e[u].y);
+            s[2] = __builtin_fmaf(s[2], d[u], e[u].z);
+            s[3] = __builtin_fmaf(s[3], d[u], e[u].w);
+        }
     }
-    *(float4 *)ws = make_float4(s[0], s[1], s[2], s[3]);
 }
 
 template <typename ET, int P, int N, int HPW>

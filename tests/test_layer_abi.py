@@ -251,7 +251,7 @@ def test_ssm_workspace(lib):  # noqa: F811
     assert ssm_size(lib, dict(s, sT=s["s0"])) == (0, 0)              # in place
     s["segment"] = 32
     slots = 100 // 32 + 3
-    need = slots * 4 * 128 * 64 * 4 + 256      # (8 bytes of decay a slot and head: 192, to 256)
+    need = slots * 4 * 128 * 64 * 4 + 256      # (4 bytes of decay a slot and head, to 256)
     assert ssm_size(lib, s) == (0, need)
     args, keep = ssm_args(s)
     assert lib.kda_ssm_prefill_ws(*args, at(20), need - 1, None) == WORKSPACE
