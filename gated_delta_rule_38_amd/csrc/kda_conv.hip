@@ -7,6 +7,8 @@
 // inputs in registers and walks a run of consecutive tokens: each input is read once (W - 1 more
 // at the start of a run), and 64 lanes move 1 KB of consecutive channels at a time.  The bound is
 // HBM: read x, write out; the arithmetic is W FMAs an element.
+#include <type_traits>
+
 #include "kda_layer.hpp"
 
 namespace kda {
@@ -131,27 +133,26 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvParams p)
                 for (int v = 0; v < V; ++v) win[k][v] = 0.f;
         }
         int m = (int)(stop - f);
-        // four inputs in flight at a time
-        for (; m >= 4; m -= 4) {
-            float in[4][V], y[V];
+        // inputs in flight: packed prefill batch, 12,288 channels: 4 at a time 332 us, 8 at a time 313,
+        // 309 with stores that bypass the caches, 16 at a time 294 (5.5 TB/s; a copy of 2 GB reaches 4.9)
+        auto steps = [&](auto count) {
+            constexpr int K = decltype(count)::value;
+            float in[K][V], y[V];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) VecIO<ET, V>::load(xp + u * p.x_st, in[u]);
+            for (int u = 0; u < K; ++u) VecIO<ET, V>::load(xp + u * p.x_st, in[u]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < K; ++u) {
                 conv_step<W, V>(win, in[u], wt, b, p.silu, y);
-                VecIO<ET, V>::store(op + u * p.o_st, y);
+                store_once<ET, V>(op + u * p.o_st, y);
             }
-            xp += 4 * p.x_st;
-            op += 4 * p.o_st;
-        }
-        for (; m > 0; --m) {
-            float in[V], y[V];
-            VecIO<ET, V>::load(xp, in);
-            conv_step<W, V>(win, in, wt, b, p.silu, y);
-            VecIO<ET, V>::store(op, y);
-            xp += p.x_st;
-            op += p.o_st;
-        }
+            xp += K * p.x_st;
+            op += K * p.o_st;
+            m -= K;
+        };
+        while (m >= 16) steps(std::integral_constant<int, 16>{});
+        if (m >= 8) steps(std::integral_constant<int, 8>{});
+        if (m >= 4) steps(std::integral_constant<int, 4>{});
+        while (m > 0) steps(std::integral_constant<int, 1>{});
         f = stop;
         if (f >= f1) return;
         ++n;

@@ -46,6 +46,22 @@ template <typename ET, int V> struct VecIO {
     }
 };
 
+// The same store for rows the launch does not read back: non-temporal where a lane writes 16 bytes.
+template <typename ET, int V>
+__device__ __forceinline__ void store_once(ET *p, const float (&f)[V])
+{
+    typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+    if constexpr (sizeof(ET) == 2 && V == 8) {
+        const u32v4 w = {pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+        __builtin_nontemporal_store(w, (u32v4 *)p);
+    } else if constexpr (sizeof(ET) == 4 && V == 4) {
+        const f32x4 w = {f[0], f[1], f[2], f[3]};
+        __builtin_nontemporal_store(w, (f32x4 *)p);
+    } else {
+        VecIO<ET, V>::store(p, f);
+    }
+}
+
 // y sigmoid(y); large negative y gives -0 (the reciprocal of an overflowed exponential).
 __device__ __forceinline__ float silu_act(float y) { return y * sigmoid_act(y); }
 

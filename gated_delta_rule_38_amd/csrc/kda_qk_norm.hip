@@ -67,44 +67,49 @@ template <typename ET, int V> struct Raw {
 template <typename ET, int V, int MODE>
 __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int lanes_log2)
 {
-    constexpr int U = 4;                            // rows in flight a lane group
-    __shared__ float2 sCS[4][128];                  // a wave's cos and sin
+    // Rows in flight a lane group.  Packed prefill batch, 40 heads: 2 rows 158 us, 4 rows 172, 8 rows 194
+    // (more registers, fewer waves); one row more requested ahead of each pair 162.
+    constexpr int U = 2;
+    constexpr bool ROT = MODE != QK_PLAIN;
+    __shared__ float2 sCS[ROT ? 4 : 1][ROT ? 128 : 1];      // a wave's cos and sin
     __shared__ __attribute__((aligned(16))) float sRow[MODE == QK_STRIP ? 4 : 1][MODE == QK_STRIP ? 64 * V : 4];
     const int wave = threadIdx.x >> 6, lane64 = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * 4 + wave;
-    const int64_t tok = item / p.splits;
-    const int split = (int)(item % p.splits);
+    const int64_t tok = p.splits == 1 ? item : item / p.splits;
+    const int split = (int)(item - tok * p.splits);
     if (tok >= p.tokens) return;
     const int64_t b = p.batched ? tok / p.T : 0, t = tok - b * p.T;
     const int lanes = 1 << lanes_log2, lane = lane64 & (lanes - 1), slot = lane64 >> lanes_log2, per = 64 >> lanes_log2;
     const int c0 = lane * V;
     const bool in = c0 < p.D;
-    const int heads0 = p.heads[0], heads = heads0 + p.heads[1], rounds = (heads + per - 1) / per;
-    const ET *xq = (const ET *)p.x[0] + b * p.x_sb[0] + t * p.x_st[0] + c0;
-    const ET *xk = (const ET *)p.x[1] + b * p.x_sb[1] + t * p.x_st[1] + c0;
-    ET *oq = (ET *)p.o[0] + b * p.o_sb[0] + t * p.o_st[0] + c0;
-    ET *ok = (ET *)p.o[1] + b * p.o_sb[1] + t * p.o_st[1] + c0;
 
     Raw<ET, V> x[U];
-    auto load = [&](int r0) {
+    // the rows of one operand: rounds r, r + splits, ... of `per` heads
+    const ET *src = nullptr;
+    int heads = 0;
+    auto load = [&](int s, int r0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int hh = (r0 + u * p.splits) * per + slot;
-            if (hh < heads && in) x[u].load(hh < heads0 ? xq + hh * p.x_sh[0] : xk + (hh - heads0) * p.x_sh[1]);
+            const int h = (r0 + u * p.splits) * per + slot;
+            if (h < heads && in) x[u].load(src + h * p.x_sh[s]);
             else
 #pragma unroll
                 for (int i = 0; i < Raw<ET, V>::W; ++i) x[u].w[i] = 0u;
         }
     };
-    load(split);
+    auto open = [&](int s) {
+        src = (const ET *)p.x[s] + b * p.x_sb[s] + t * p.x_st[s] + c0;
+        heads = p.heads[s];
+    };
+    open(0);
+    load(0, split);
 
-    // this lane's pairs: cos, sin with the sign its channels take it with
+    // this lane's pairs: cos, and sin with the sign its channels take the partner with
     const int half = p.rot >> 1, i0 = c0 - p.offset;
-    constexpr int NP = MODE == QK_INTER ? V / 2 : V;
-    float cs[MODE == QK_PLAIN ? 1 : NP], sn[MODE == QK_PLAIN ? 1 : NP];
+    float cs[ROT ? V : 1], sn[ROT ? V : 1];
     int partner = lane64;
     bool turns = false;
-    if constexpr (MODE != QK_PLAIN) {
+    if constexpr (ROT) {
         const double pos = (double)p.pos[b * p.pos_sb + t * p.pos_st] * 0.15915494309189533577;     // 1 / (2 pi)
         for (int e = lane64; e < half; e += 64) {
             const double a = pos * (double)p.freq[e];
@@ -114,81 +119,93 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int 
         }
         __builtin_amdgcn_wave_barrier();            // one wave's LDS accesses keep their order
 #pragma unroll
-        for (int v = 0; v < NP; ++v) {
-            // channel of pair v: whether it is rotated, and its pair
-            const int i = MODE == QK_INTER ? i0 + 2 * v : i0 + v;
-            const bool rot = i >= 0 && i < p.rot, first = i < half;
+        for (int v = 0; v < V; ++v) {
+            const int i = i0 + v;
+            const bool rot = i >= 0 && i < p.rot, first = MODE == QK_INTER ? !(i & 1) : i < half;
             const int e = MODE == QK_INTER ? i >> 1 : (first ? i : i - half);
             const float2 q = sCS[wave][rot ? e : 0];
             cs[v] = rot ? q.x : 1.f;
-            sn[v] = rot ? (MODE != QK_INTER && first ? -q.y : q.y) : 0.f;
+            sn[v] = rot ? (first ? -q.y : q.y) : 0.f;
         }
         if constexpr (MODE == QK_LANES) {
             turns = i0 >= 0 && i0 < p.rot;
             if (turns) partner = lane64 + (i0 < half ? half : -half) / V;
         }
     }
-    // norm weights of this lane's channels, and of its partner's
-    float wt[2][V], wp[MODE == QK_LANES ? 2 : 1][MODE == QK_LANES ? V : 1];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
+
+    for (int s = 0; s < 2; ++s) {
+        if (s) {
+            open(1);
+            load(1, split);
+        }
+        if (heads == 0) continue;
+        ET *dst = (ET *)p.o[s] + b * p.o_sb[s] + t * p.o_st[s] + c0;
+        // out = rn (own A + partner B): the norm weights (own, partner's) and the rotation in one
+        float A[V], B[ROT ? V : 1];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            wt[s][v] = (p.w[s] && in) ? p.w[s][c0 + v] : 1.f;
-            if constexpr (MODE == QK_LANES) wp[s][v] = (p.w[s] && in) ? p.w[s][(partner - lane64) * V + c0 + v] : 1.f;
+            const float w = (p.w[s] && in) ? p.w[s][c0 + v] : 1.f;
+            A[v] = ROT ? w * cs[ROT ? v : 0] : w;
+            if constexpr (ROT) {
+                const int i = i0 + v;
+                int far = c0 + v;
+                if (i >= 0 && i < p.rot) far += MODE == QK_INTER ? ((i & 1) ? -1 : 1) : (i < half ? half : -half);
+                B[v] = ((p.w[s] && in) ? p.w[s][far] : 1.f) * sn[v];
+            }
         }
-
-    for (int r0 = split; r0 < rounds; r0 += U * p.splits) {
-        if (r0 != split) load(r0);
+        const int rounds = (heads + per - 1) / per;
+        for (int r0 = split; r0 < rounds; r0 += U * p.splits) {
+            if (r0 != split) load(s, r0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int hh = (r0 + u * p.splits) * per + slot;
-            if (r0 + u * p.splits >= rounds) break;     // the same for the whole wave
-            const int s = hh >= heads0;
-            float y[V], other[V];
-            x[u].unpack(y);
-            if constexpr (MODE == QK_LANES) {
-                Raw<ET, V> far;
+            for (int u = 0; u < U; ++u) {
+                if (r0 + u * p.splits >= rounds) break;     // the same for the whole wave
+                const int h = (r0 + u * p.splits) * per + slot;
+                float y[V];
+                x[u].unpack(y);
+                float rn = 1.f;
+                if (p.norm) {
+                    float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < Raw<ET, V>::W; ++i)
-                    far.w[i] = __builtin_amdgcn_ds_bpermute(partner << 2, x[u].w[i]);
-                far.unpack(other);
-            }
-            if (p.norm) {
-                float ss = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) ss = __builtin_fmaf(y[v], y[v], ss);
-                ss = group_sum(ss, lanes);
-                const float rn = 1.f / sqrtf(__builtin_fmaf(ss, p.inv_d, p.eps));
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    y[v] *= rn * (s ? wt[1][v] : wt[0][v]);
-                    if constexpr (MODE == QK_LANES) other[v] *= rn * (s ? wp[1][v] : wp[0][v]);
+                    for (int v = 0; v < V; ++v) ss = __builtin_fmaf(y[v], y[v], ss);
+                    rn = __builtin_amdgcn_rsqf(__builtin_fmaf(group_sum(ss, lanes), p.inv_d, p.eps));
                 }
-            }
-            if constexpr (MODE == QK_INTER) {
+                float z[V];
+                if constexpr (MODE == QK_PLAIN) {
 #pragma unroll
-                for (int v = 0; v < V / 2; ++v) {
-                    const float a = y[2 * v], c = y[2 * v + 1];
-                    y[2 * v] = a * cs[v] - c * sn[v];
-                    y[2 * v + 1] = c * cs[v] + a * sn[v];
+                    for (int v = 0; v < V; ++v) z[v] = y[v] * A[v];
+                } else if constexpr (MODE == QK_INTER) {
+#pragma unroll
+                    for (int v = 0; v < V; v += 2) {
+                        // a pair that does not turn takes nothing of each other, not even a NaN
+                        const bool rot = i0 + v >= 0 && i0 + v < p.rot;
+                        z[v] = rot ? __builtin_fmaf(y[v + 1], B[v], y[v] * A[v]) : y[v] * A[v];
+                        z[v + 1] = rot ? __builtin_fmaf(y[v], B[v + 1], y[v + 1] * A[v + 1]) : y[v + 1] * A[v + 1];
+                    }
+                } else if constexpr (MODE == QK_LANES) {
+                    Raw<ET, V> far;
+                    float other[V];
+#pragma unroll
+                    for (int i = 0; i < Raw<ET, V>::W; ++i) far.w[i] = __builtin_amdgcn_ds_bpermute(partner << 2, x[u].w[i]);
+                    far.unpack(other);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) z[v] = turns ? __builtin_fmaf(other[v], B[v], y[v] * A[v]) : y[v] * A[v];
+                } else {
+                    float *strip = sRow[wave] + slot * (lanes * V);
+#pragma unroll
+                    for (int v = 0; v < V; v += 4) *(float4 *)(strip + c0 + v) = make_float4(y[v], y[v + 1], y[v + 2], y[v + 3]);
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int i = i0 + v;
+                        z[v] = y[v] * A[v];
+                        if (i >= 0 && i < p.rot) z[v] = __builtin_fmaf(strip[c0 + v + (i < half ? half : -half)], B[v], z[v]);
+                    }
+                    __builtin_amdgcn_wave_barrier();
                 }
-            } else if constexpr (MODE == QK_LANES) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) y[v] = turns ? y[v] * cs[v] + other[v] * sn[v] : y[v];
-            } else if constexpr (MODE == QK_STRIP) {
-                float *strip = sRow[wave] + slot * (lanes * V);
-#pragma unroll
-                for (int v = 0; v < V; v += 4) *(float4 *)(strip + c0 + v) = make_float4(y[v], y[v + 1], y[v + 2], y[v + 3]);
-                __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int i = i0 + v;
-                    if (i >= 0 && i < p.rot) y[v] = y[v] * cs[v] + strip[c0 + v + (i < half ? half : -half)] * sn[v];
-                }
-                __builtin_amdgcn_wave_barrier();
+                for (int v = 0; v < V; ++v) z[v] *= rn;
+                if (h < heads && in) store_once<ET, V>(dst + h * p.o_sh[s], z);
             }
-            if (hh < heads && in) VecIO<ET, V>::store(s ? ok + (hh - heads0) * p.o_sh[1] : oq + hh * p.o_sh[0], y);
         }
     }
 }
