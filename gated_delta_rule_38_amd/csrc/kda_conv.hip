@@ -204,11 +204,11 @@ __global__ __launch_bounds__(256) void conv_decode_kernel(const ConvDecodeParams
         float in[V], y[V];
         VecIO<ET, V>::load(x + t * p.x_st, in);
         conv_step<W, V>(win, in, wt, b, p.silu, y);
-        if (o) VecIO<ET, V>::store(o + t * p.o_st, y);
+        if (o) store_once<ET, V>(o + t * p.o_st, y);
     }
     if (p.update && n > 0) {
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) VecIO<ST, V>::store(ps + k * p.p_sr, win[k]);
+        for (int k = 0; k < W - 1; ++k) store_once<ST, V>(ps + k * p.p_sr, win[k]);
     }
 }
 
