@@ -608,6 +608,8 @@ kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_
     for (int64_t stride : {s.x.st, s.B.st, s.C.st, s.z.st, s.out.st})
         if (stride > ((int64_t)1 << 31) / (kda::SSM_CHUNK * 4) - 256)
             return fail(KDA_ERR_UNSUPPORTED, "token strides must stay below 2^24 - 256 elements");
+    if (s.H > 1 && (s.x.s1 > (int64_t)1 << 28 || s.z.s1 > (int64_t)1 << 28))
+        return fail(KDA_ERR_UNSUPPORTED, "head strides of x and z must stay within 2^28 elements");
     const Named ins[] = {{x, "x"}, {dt, "dt"}, {A, "A"}, {B, "B"}, {C, "C"}, {s0, "initial_state"}, {cu, "cu_seqlens"},
                          {s.tD, "D"}, {s.tbias, "dt_bias"}, {s.tz, "z"}};
     KDA_TRY(no_overlap(out, "out", ins));

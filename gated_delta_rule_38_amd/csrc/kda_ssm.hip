@@ -423,7 +423,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
         bool direct = false;
         for (int c = 0; c < GC; ++c) {
             const double tot = sum_of(sSum[k & 1][c][u.h][L - 1]), old = base;
-            const bool d = tot < -LIMIT, move = base + tot < -LIMIT && base != 0.;
+            const bool d = tot < -LIMIT, move = fabs(base + tot) > LIMIT && base != 0.;
             if (move) base = 0.;
             if (c == u.c) {
                 mine = base;

@@ -130,9 +130,10 @@ int64_t extent(const at::Tensor &t, int64_t d)      // negative d: from the end;
     return d >= 0 && d < t.dim() ? t.size(d) : 0;
 }
 
-int64_t sequences(const at::Tensor &cu, const at::Tensor &x)
+// Sequences of a batch whose dense layout has `dims` dimensions (0 where the call will be refused).
+int64_t sequences(const at::Tensor &cu, const at::Tensor &x, int64_t dims)
 {
-    return cu.defined() ? (cu.numel() > 0 ? cu.numel() - 1 : 0) : extent(x, 0);
+    return cu.defined() ? (cu.numel() > 0 ? cu.numel() - 1 : 0) : x.dim() == dims ? x.size(0) : 0;
 }
 
 template <typename F>
@@ -167,7 +168,7 @@ PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n)
         for (size_t i = 0; i < 7; ++i) c.put(i, a[i]);
         if (!c.has(5)) c.make(5, c.t[0].sizes(), c.t[0].scalar_type());
         if (!c.has(6) && PyObject_IsTrue(a[7]) && c.has(1))
-            c.make(6, {sequences(c.t[4], c.t[0]), std::max<int64_t>(0, extent(c.t[1], -1) - 1), extent(c.t[0], -1)},
+            c.make(6, {sequences(c.t[4], c.t[0], 3), std::max<int64_t>(0, extent(c.t[1], -1) - 1), extent(c.t[0], -1)},
                    (c.has(3) ? c.t[3] : c.t[0]).scalar_type());
         const int act = (int)PyLong_AsLong(a[8]);
         void *s = c.stream();
@@ -232,7 +233,7 @@ PyObject *ssm_prefill(PyObject *, PyObject *const *a, Py_ssize_t n)
         for (size_t i = 0; i < 12; ++i) c.put(i, a[i]);
         if (!c.has(7)) c.make(7, c.t[0].sizes(), c.t[0].scalar_type());
         if (!c.has(8) && PyObject_IsTrue(a[13]) && c.has(3))
-            c.make(8, {sequences(c.t[6], c.t[0]), extent(c.t[0], -2), extent(c.t[3], -1), extent(c.t[0], -1)}, at::kFloat);
+            c.make(8, {sequences(c.t[6], c.t[0], 4), extent(c.t[0], -2), extent(c.t[3], -1), extent(c.t[0], -1)}, at::kFloat);
         const kda_ssm_options_t o = ssm_options(c.at(9), c.at(10), c.at(11), a[14], a[15]);
         size_t need = 0;
         run([&] { return api.ssm_size(c.at(0), c.at(1), c.at(2), c.at(3), c.at(4), c.at(5), c.at(6), c.at(7), c.at(8), &o, &need); });

@@ -34,8 +34,9 @@ enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 };
  * x, out: dense [B, T, C] or packed [T, C] / [1, T, C] with cu_seqlens; bf16 or fp32 alike.
  * weight [C, W], W in 2..4, and bias [C] (or NULL): each bf16 or fp32; weight is contiguous.
  * States [N, W - 1, C], each bf16 or fp32 (x is kept exactly in x's dtype).
- * out may not overlap any input; final_state may be exactly initial_state (same view), or must
- * not overlap any input.  Sums in fp32, one rounding to out's dtype.
+ * out may not overlap any input; final_state may be exactly initial_state (same view; one more small
+ * launch), or must not overlap any input.  Sums in fp32, one rounding to out's dtype.  Rows behind
+ * cu[N] are not read and left as they were.
  */
 kda_status_t kda_conv(const kda_tensor_t *x, const kda_tensor_t *weight, const kda_tensor_t *bias,
                       const kda_tensor_t *initial_state, const kda_tensor_t *cu_seqlens, kda_tensor_t *out,
@@ -105,12 +106,15 @@ typedef struct {
  * x, z, out: dense [B, T, H, P] or packed [T, H, P] / [1, T, H, P]; dt: [.., H], x's dtype or fp32;
  * A: fp32 [H]; B, C: [.., G, N], head h reading group h / (H / G).  P and N each 64 or 128; G
  * divides H.  x, B, C, z, out all bf16, or all fp32.  States [n, H, N, P], fp32 or bf16 each; the
- * state is carried in fp32 or better in between.  A <= 0 with steps >= 0 is the method's range;
- * other signs follow the same formula as far as fp32's range goes.
+ * state is carried in fp32 or better in between.  A and steps finite, A step <= 0 (a growing head,
+ * A step > 0, follows the same formula while a chunk grows by less than 2^96).
  * Chunks of 32 tokens run on the matrix cores.  On bf16 data products of inputs are exact, the
- * state's additive term keeps 24 bits, and the state and the decay matrix are rounded to bf16
- * where they only feed out.  A NaN or infinity in x at a token can reach the outputs of up to 31
- * tokens before it in its sequence, never another sequence or head.
+ * state's additive term keeps 24 bits, and the state and the products of B and C are rounded to bf16
+ * where they only feed out.  Terms are weighted by up to 2^96 against each other, so |x B C| (and
+ * their sums) may reach 2^31.  A NaN or infinity in x or dt at a token can reach the outputs of up to
+ * 31 tokens before it in its sequence, never another sequence, and only its own head.
+ * Rows behind cu[N] are not read and left as they were.  Token strides below 2^24 - 256 elements and
+ * head strides of x and z within 2^28.
  * Uses the library's cached workspace like kda_prefill; kda_ssm_prefill_ws takes the caller's
  * (256-byte aligned, kda_ssm_workspace_size() bytes, NULL when 0), allocates nothing and can be
  * captured.  out may not overlap any input; final_state may be exactly initial_state.

@@ -451,6 +451,67 @@ def test_ssm_empty_and_behind(kda):
     assert torch.equal(none[1], c["initial_state"])
 
 
+def test_ssm_cached_workspace_entry(kda):
+    """kda_ssm_prefill (the library's own workspace) gives kda_ssm_prefill_ws's bits, twice in a row,
+    the second time with a smaller batch."""
+    import ctypes
+
+    import torch
+
+    from test_layer_abi import SsmOptions
+    lib = kda.load_library()
+    for lengths in ([500, 130], [200]):
+        c = ssm_case(lengths, 2, 1, 64, 128, "bf16", seed=len(lengths))
+        want, wf = kda.ssm_prefill(**c, segment=64)
+        out, fin = torch.full_like(want, float("nan")), torch.full_like(wf, float("nan"))
+        ds = {k: kda.describe(v) for k, v in c.items() if isinstance(v, torch.Tensor)}
+        ds["out"], ds["final"] = kda.describe(out), kda.describe(fin)
+        a = {k: ctypes.addressof(d) for k, d in ds.items()}
+        o = SsmOptions(a["D"], a["dt_bias"], a["z"], 1, 64)
+        st = lib.kda_ssm_prefill(a["x"], a["dt"], a["A"], a["B"], a["C"], a["initial_state"], a["cu_seqlens"], a["out"],
+                                 a["final"], ctypes.addressof(o), torch.cuda.current_stream().cuda_stream)
+        assert st == 0, lib.kda_last_error()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want)) and torch.equal(fin, wf)
+    kda.release_cached_workspace()
+
+
+def test_ssm_nan_stays_in_its_sequence_and_head(kda):
+    """A NaN in x or dt reaches its own sequence and head alone, later tokens for certain and at most 31
+    tokens before; one in C its own token alone."""
+    import torch
+    c = ssm_case([100, 90], 4, 1, 64, 64, "bf16", seed=15)
+    clean, cf = kda.ssm_prefill(**c, segment=-1)
+    for key, at in (("x", (50, 1, 7)), ("dt", (50, 1))):
+        bad = dict(c, **{key: c[key].clone()})
+        bad[key][at] = float("nan")
+        for seg in (-1, 32):
+            out, fin = kda.ssm_prefill(**bad, segment=seg)
+            ref_out, ref_fin = kda.ssm_prefill(**c, segment=seg)
+            assert torch.equal(bits(out[100:]), bits(ref_out[100:])) and torch.equal(fin[1], ref_fin[1])
+            heads = [0, 2, 3]
+            assert torch.equal(bits(out[:, heads]), bits(ref_out[:, heads])) and torch.equal(fin[:, heads], ref_fin[:, heads])
+            cols = [7] if key == "x" else list(range(64))
+            assert torch.isnan(out[50:100, 1][:, cols]).all() and torch.isnan(fin[0, 1][:, cols]).all()
+            assert torch.equal(bits(out[:32]), bits(ref_out[:32]))
+    bad = dict(c, C=c["C"].clone())
+    bad["C"][50, 0, 3] = float("nan")
+    out, fin = kda.ssm_prefill(**bad, segment=-1)
+    keep = [t for t in range(190) if t != 50]
+    assert torch.isnan(out[50]).all() and torch.equal(bits(out[keep]), bits(clean[keep])) and torch.equal(fin, cf)
+
+
+def test_ssm_growth_and_long_decay(kda):
+    """Heads that grow (A step > 0), and references that move many times: slow decay over 3,000 tokens,
+    against the float64 recurrence."""
+    c = ssm_case([3000], 3, 1, 64, 64, "f32", seed=19, gate=False, softplus=False)
+    c["A"][0], c["A"][1], c["A"][2] = 0.2, -0.5, -30.0
+    c["dt"][:, 0] *= 0.1
+    for seg in (-1, 512):
+        out, fin = kda.ssm_prefill(**c, segment=seg)
+        check_ssm(c, out, fin, "f32")
+
+
 @pytest.mark.parametrize("T", [1, 3, 8])
 @pytest.mark.parametrize("H,G,P,N", [(2, 1, 64, 128), (4, 2, 64, 64), (3, 1, 128, 64), (2, 2, 128, 128)])
 @pytest.mark.parametrize("dtype,state", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
@@ -523,6 +584,48 @@ def test_ssm_prompt_then_decode_and_conv(kda):
 
 
 # ------------------------------------------------------------------ streams, graphs, shared use
+
+def test_layer_calls_from_two_streams_at_once(kda):
+    """The same segmented scan in flight on two streams at once (each with its own workspace): both
+    give the lone call's bits."""
+    import torch
+    c = ssm_case([900, 400], 4, 1, 64, 128, "bf16", seed=71)
+    want, wf = kda.ssm_prefill(**c, segment=64)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [kda.ssm_prefill(**c, segment=64, stream=s) for _ in range(5) for s in streams]
+    for s in streams:
+        s.synchronize()
+    for out, fin in got:
+        assert torch.equal(bits(out), bits(want)) and torch.equal(fin, wf)
+
+
+def test_layer_large_offsets(kda):
+    """Tensors past 2^31 elements (5 GB of x): the last rows are right."""
+    import torch
+    rows, C = 17 * 4096, 32768          # 2.28e9 elements
+    x = torch.zeros(rows, C, dtype=torch.bfloat16, device="cuda")
+    d = Draw(81)
+    x[-40:] = d.randn(40, C, dtype="bf16")
+    w = d.randn(C, 4, dtype="bf16")
+    out = torch.full((rows, C), -512.0, dtype=torch.bfloat16, device="cuda")
+    kda.conv(x, w, cu_seqlens=ints([0, rows]), out=out, activation="silu", output_final_state=False)
+    want, _ = kda.conv(x[-40:].contiguous(), w, cu_seqlens=ints([0, 40]), activation="silu")
+    assert torch.equal(bits(out[-40:]), bits(want)) and (out[:rows - 40] == 0).all()
+    q = x.view(rows, C // 128, 128)
+    qo, _ = kda.qk_norm(q, norm="l2", q_out=out.view(rows, C // 128, 128))
+    small, _ = kda.qk_norm(q[-40:].contiguous(), norm="l2")
+    assert torch.equal(bits(qo[-40:]), bits(small))
+    H = C // 64 // 2
+    xs = x[:, :H * 64].unflatten(1, (H, 64))                # rows 2 x the width apart
+    c = dict(dt=torch.zeros(rows, H, device="cuda"), A=-torch.ones(H, device="cuda"), B=d.randn(rows, 1, 64, dtype="bf16"),
+             C=d.randn(rows, 1, 64, dtype="bf16"), D=None, dt_bias=None, z=None, initial_state=None, dt_softplus=True)
+    ys, fs = kda.ssm_prefill(xs, **c, cu_seqlens=ints([0, rows]))
+    # the tokens before the last 40 add nothing, so the last 64 alone have the same result
+    tail = {k: (v[-64:].contiguous() if k in ("dt", "B", "C") else v) for k, v in c.items()}
+    check_ssm(dict(tail, x=xs[-64:].contiguous(), cu_seqlens=ints([0, 64])), ys[-64:], fs, "bf16")
+    assert (ys[:rows - 64] == 0).all()
+
 
 def test_layer_on_other_stream_and_in_a_graph(kda):
     """The whole step on a stream of its own, then captured and replayed on changed inputs, with
