@@ -523,9 +523,9 @@ double ssm_pass(double workgroups, double chunks, double alone, double shared, b
 // into start states, read: 2.35 TB/s) and the scan's walk; 2.4 times as much a chunk in fp32.  The
 // lengths of a packed batch are on the device: a whole run is charged a longest sequence of 1.7 times
 // the mean, whose end it runs alone, and segments half a segment of waste a sequence.
-// On 15 batches of 203 to 65,536 tokens and 4 to 64 heads, against 5 to 16 forced lengths each, the
-// choice is within 7% of the best but for one packed batch (16% and more where its few lengths fit a
-// round of workgroups exactly, which the host cannot see).
+// On 22 batches of 203 to 65,536 tokens and 4 to 64 heads, against 5 to 16 forced lengths each, the
+// choice is within 9% of the best but for five packed batches (15 to 28%, where a length happens to
+// fill whole rounds of workgroups, which the host cannot see).
 void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32)
 {
     const int64_t hg = s.H / s.G;
@@ -552,7 +552,7 @@ void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32)
             }
         }
     }
-    if (s.seg >= longest) s.seg = 0;
+    if (s.seg >= longest || N == 0) s.seg = 0;
     if (s.seg == 0) {
         s.slots = N;
         return;
@@ -606,7 +606,7 @@ kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_
         if (!aligned_to(t, 4)) return fail(KDA_ERR_LAYOUT, "x, B, C, z and out need 4-element-aligned base addresses and strides");
     // the kernel addresses a chunk of each with 32-bit byte offsets from its first row
     for (int64_t stride : {s.x.st, s.B.st, s.C.st, s.z.st, s.out.st})
-        if (stride > ((int64_t)1 << 31) / (kda::SSM_CHUNK * 4) - 256)
+        if ((s.L.dense ? s.L.T : s.L.tokens) > 1 && stride > ((int64_t)1 << 31) / (kda::SSM_CHUNK * 4) - 256)
             return fail(KDA_ERR_UNSUPPORTED, "token strides must stay below 2^24 - 256 elements");
     if (s.H > 1 && (s.x.s1 > (int64_t)1 << 28 || s.z.s1 > (int64_t)1 << 28))
         return fail(KDA_ERR_UNSUPPORTED, "head strides of x and z must stay within 2^28 elements");

@@ -57,6 +57,8 @@ def _on(stream, x):
     import torch
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    elif stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
     return torch.cuda.stream(stream)
 
 
@@ -176,7 +178,8 @@ def ssm_prefill(x, dt, A, B, C, D=None, dt_bias=None, z=None, initial_state=None
     step = softplus(dt + dt_bias) (``dt_softplus``) or dt + dt_bias:
         S_t = exp(A step_t) S_{t-1} + step_t B_t x_t^T,   out = (S_t^T C_t + D x_t) silu(z_t).
     States [N_seq, H, N, P]; a final state allocated here is fp32.  ``workspace``: an optional uint8
-    tensor of at least ``ssm_workspace_size`` + 256 bytes; by default torch allocates one.
+    tensor of at least ``ssm_workspace_size`` + 256 bytes, of one call in flight at a time; by default
+    torch allocates one.
     """
     args = (x, dt, A, B, C, initial_state, cu_seqlens, out, final_state, D, dt_bias, z, workspace, output_final_state,
             dt_softplus, segment)

@@ -94,7 +94,7 @@ typedef struct {
     const kda_tensor_t *dt_bias;  /* [H]: added to dt                                             */
     const kda_tensor_t *z;        /* out's shape and dtype: out = y silu(z)                       */
     int32_t dt_softplus;          /* 1: the step is softplus(dt + dt_bias)                        */
-    int32_t segment;              /* prefill: tokens per segment, a multiple of 32; 0 = planner's */
+    int32_t segment;              /* prefill: tokens per segment, a multiple of 32; 0 = planner's, -1 = whole sequences */
                                   /* choice, -1 = whole sequences                                 */
 } kda_ssm_options_t;
 

@@ -451,6 +451,41 @@ def test_ssm_empty_and_behind(kda):
     assert torch.equal(none[1], c["initial_state"])
 
 
+@pytest.mark.parametrize("lengths", [[64, 64, 0, 128, 65, 63, 1], [192, 96, 96], [0, 0, 31, 0], [97, 1, 1, 1, 127]])
+@pytest.mark.parametrize("behind", [0, 70])
+def test_ssm_segments_of_packed_batches(kda, lengths, behind):
+    """Lengths at and around multiples of the segment, empty sequences, rows behind the last one (not
+    read: they hold NaN; left as they were)."""
+    import torch
+    rows = sum(lengths)
+    c = ssm_case(lengths, 2, 1, 64, 64, "bf16", seed=rows + behind)
+    want = ssm_ref(c)
+    for seg in (32, 64, 96):
+        call = dict(c)
+        for key in ("x", "dt", "B", "C", "z"):
+            pad = torch.full((behind, *c[key].shape[1:]), float("nan"), dtype=c[key].dtype, device="cuda")
+            call[key] = torch.cat([c[key], pad])
+        out = torch.full_like(call["x"], -7.0)
+        _, fin = kda.ssm_prefill(**call, out=out, segment=seg)
+        check_ssm(c, out[:rows], fin, "bf16", want=want)
+        assert (out[rows:] == -7.0).all()
+
+
+def test_layer_without_sequences(kda):
+    """cu_seqlens of no sequence: nothing is read or written."""
+    import torch
+    c = ssm_case([80], 2, 1, 64, 64, "bf16", seed=3, full=False)
+    c["cu_seqlens"] = ints([0])
+    for seg in (0, -1, 32):
+        out = torch.full_like(c["x"], -7.0)
+        _, fin = kda.ssm_prefill(**c, out=out, segment=seg)
+        assert (out == -7.0).all() and fin.shape == (0, 2, 64, 64)
+    x = Draw(1).randn(80, 16, dtype="bf16")
+    out = torch.full_like(x, -7.0)
+    _, fin = kda.conv(x, Draw(2).randn(16, 4, dtype="bf16"), cu_seqlens=ints([0]), out=out)
+    assert (out == -7.0).all() and fin.shape == (0, 3, 16)
+
+
 def test_ssm_cached_workspace_entry(kda):
     """kda_ssm_prefill (the library's own workspace) gives kda_ssm_prefill_ws's bits, twice in a row,
     the second time with a smaller batch."""

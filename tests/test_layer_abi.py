@@ -334,3 +334,12 @@ def test_layer_binding_refuses_without_gpu():
         kda.conv(x, w, activation="relu")
     with pytest.raises(ValueError):
         kda.qk_norm(x, norm="layer")
+
+
+def test_ssm_without_sequences_needs_no_workspace(lib):
+    """Rows without any sequence: nothing to cut, whatever segment is asked for."""
+    s = ssm_set()
+    s["cu"] = desc([1], KDA_I32, at(6))
+    s["s0"] = s["sT"] = None
+    s["segment"] = 32
+    assert ssm_size(lib, s) == (0, 0)
