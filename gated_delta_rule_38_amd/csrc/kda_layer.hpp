@@ -155,6 +155,7 @@ struct SsmParams {
     int32_t dt_bf16, softplus, s0_bf16, sT_bf16;
     int32_t seg;               // tokens per segment (a multiple of SSM_CHUNK); 0: whole sequences
     int32_t slots;             // segment slots (seg > 0) or sequences: the last N for last segments
+    int32_t own_start;         // workgroups form their own start states (else the scan did)
     int32_t wg_per_slot;       // workgroups of one slot
     int32_t heads_per_wg;
     int32_t wide;              // x, z, B, C rows are 16-byte aligned (else 8-byte, bf16)

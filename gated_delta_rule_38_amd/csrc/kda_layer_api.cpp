@@ -471,6 +471,7 @@ struct Ssm {
     const kda_tensor_t *tD = nullptr, *tbias = nullptr, *tz = nullptr;
     int32_t softplus = 0;
     int64_t seg = 0, slots = 0;
+    bool own_start = false;
     int hpw = 1;
     int64_t wps = 0;
     size_t off_decay = 0, bytes = 0;
@@ -519,14 +520,19 @@ double ssm_pass(double workgroups, double chunks, double alone, double shared, b
 
 // Segment length of a batch (0: whole sequences), by a cost in microseconds fitted to MI355X.  Whole
 // sequences: one pass.  Segments: the states' pass (1.4 us a chunk, shared or not), the outputs' pass
-// (2.3 alone, 4.3 shared, 3.7 with 64 state channels), the states' way through memory (written, turned
-// into start states, read: 2.35 TB/s) and the scan's walk; 2.4 times as much a chunk in fp32.  The
-// lengths of a packed batch are on the device: a whole run is charged a longest sequence of 1.7 times
-// the mean, whose end it runs alone, and segments half a segment of waste a sequence.
-// On 22 batches of 203 to 65,536 tokens and 4 to 64 heads, against 5 to 16 forced lengths each, the
-// choice is within 9% of the best but for five packed batches (15 to 28%, where a length happens to
-// fill whole rounds of workgroups, which the host cannot see).
-void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32)
+// (2.3 alone, 4.3 shared, 3.7 with 64 state channels), and the way from end states to start states; 2.4
+// times as much a chunk in fp32.  That way is the shorter of two.  The scan, a launch: end states
+// written, turned into start states, read again (2.35 TB/s), and its walk.  Or every workgroup of the
+// outputs' pass reads the end states before its own (16 TB/s, mostly from caches): no launch and no
+// second trip, but bytes that grow with the segments of a sequence (8 prompts, 32,733 tokens, segments
+// of 1,536: 420 us with the scan, 400 without; one of 65,536 in segments of 1,024: 180 and 212).
+// The lengths of a packed batch are on the device: a whole run is charged a longest sequence of 1.7
+// times the mean, whose end it runs alone, and segments half a segment of waste a sequence.
+// On 8 batches of 203 to 65,536 tokens and 4 to 64 heads against 8 forced lengths each the choice is
+// within 10% of the best; on random packed batches up to 28% (where a length happens to fill whole
+// rounds of workgroups, which the host cannot see).
+// in_place: the final states replace the initial ones, which other workgroups would still read.
+void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32, bool in_place)
 {
     const int64_t hg = s.H / s.G;
     s.hpw = s.P == 64 && hg > 1 ? 2 : 1;
@@ -534,18 +540,26 @@ void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32)
     const int64_t N = s.L.N, longest = s.L.dense ? s.L.T : s.L.tokens;    // the longest a sequence can be
     const int asked = o ? o->segment : 0;
     s.seg = std::max(0, asked);
+    const double T = (double)s.L.tokens, n = (double)N, cl = kda::SSM_CHUNK;
+    const double likely = s.L.dense || N == 1 ? (double)longest : std::min((double)longest, 1.7 * T / n);
+    // segments of a length, and the cost of their start states
+    auto count = [&](int64_t seg) { return s.L.dense || N == 1 ? n * std::ceil((double)longest / (double)seg) : T / (double)seg + 0.5 * n; };
+    auto starts = [&](int64_t seg, bool &own) {
+        const double bytes = std::max(0., count(seg) - n) * (double)s.H * (double)(s.N * s.P) * 4., each = likely / (double)seg;
+        const double scan = 2. * bytes / 2.35e6 + 0.03 * each + 10., walk = bytes / 5e6 + 0.5 * each * bytes / 16e6;
+        own = !in_place && walk < scan;
+        return own ? walk : scan;
+    };
     if (asked == 0 && N > 0 && longest > kda::SSM_CHUNK) {
-        const double cl = kda::SSM_CHUNK, per = f32 ? 2.4 : 1., shared = s.N == 64 ? 3.7 : 4.3;
+        const double per = f32 ? 2.4 : 1., shared = s.N == 64 ? 3.7 : 4.3;
         const double half = s.P == 64 && s.hpw == 1 ? 0.5 : 1.;     // (workgroups of half the size)
-        const double T = (double)s.L.tokens, n = (double)N, wgs = (double)s.wps * half;
-        const double likely = s.L.dense || N == 1 ? (double)longest : std::min((double)longest, 1.7 * T / n);
-        const double mean = std::ceil(T / n / cl);
+        const double wgs = (double)s.wps * half, mean = std::ceil(T / n / cl);
         double best = per * (ssm_pass(n * wgs, mean, 2.3, shared, f32) + (std::ceil(likely / cl) - mean) * 2.3);
         for (int64_t seg = 32; seg < longest && seg <= 8192; seg += seg < 256 ? 32 : seg < 1024 ? 128 : 256) {
-            const double segs = s.L.dense || N == 1 ? n * std::ceil((double)longest / (double)seg) : T / (double)seg + 0.5 * n;
-            const double chunks = (double)seg / cl, states = std::max(0., segs - n) * (double)s.H * (double)(s.N * s.P) * 8.;
+            const double segs = count(seg), chunks = (double)seg / cl;
+            bool own;
             const double cost = per * (ssm_pass((segs - n) * wgs, chunks, 1.4, 1.4, f32) + ssm_pass(segs * wgs, chunks, 2.3, shared, f32)) +
-                                states / 2.35e6 + 0.03 * likely / (double)seg;
+                                starts(seg, own);
             if (cost < best) {
                 best = cost;
                 s.seg = seg;
@@ -557,6 +571,7 @@ void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32)
         s.slots = N;
         return;
     }
+    starts(s.seg, s.own_start);
     s.slots = s.L.dense ? N * std::max<int64_t>(1, (s.L.T + s.seg - 1) / s.seg) : s.L.tokens / s.seg + N;
     s.off_decay = align256((size_t)s.slots * s.H * s.N * s.P * 4);
     s.bytes = s.off_decay + align256((size_t)s.slots * s.H * 4);
@@ -617,13 +632,13 @@ kda_status_t ssm_check(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_
     if (sT && overlaps(span_of(sT), span_of(out))) return fail(KDA_ERR_ALIAS, "final_state overlaps out");
     KDA_TRY(distinct_rows(out, "out"));
     KDA_TRY(distinct_rows(sT, "final_state"));
-    ssm_plan(s, o, x->dtype == KDA_F32);
+    ssm_plan(s, o, x->dtype == KDA_F32, s0 && sT && s0->data == sT->data);
     if (s.slots * s.wps > (int64_t)INT32_MAX || s.L.N * s.H * (s.N * s.P / 1024) > (int64_t)INT32_MAX)
         return fail(KDA_ERR_UNSUPPORTED, "too many workgroups for one launch");
     if (env_on("KDA_LOG"))
-        fprintf(stderr, "kda: ssm plan N=%lld tokens=%lld H=%lld G=%lld P=%lld N=%lld segment=%lld slots=%lld workgroups=%lld workspace=%zu B\n",
+        fprintf(stderr, "kda: ssm plan N=%lld tokens=%lld H=%lld G=%lld P=%lld N=%lld segment=%lld slots=%lld workgroups=%lld workspace=%zu B%s\n",
                 (long long)s.L.N, (long long)s.L.tokens, (long long)s.H, (long long)s.G, (long long)s.P, (long long)s.N,
-                (long long)s.seg, (long long)s.slots, (long long)(s.slots * s.wps), s.bytes);
+                (long long)s.seg, (long long)s.slots, (long long)(s.slots * s.wps), s.bytes, s.own_start ? ", own start states" : "");
     return KDA_OK;
 }
 
@@ -649,7 +664,7 @@ kda_status_t ssm_run(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_te
     p.N = (int32_t)s.L.N; p.T = (int32_t)s.L.T; p.H = (int32_t)s.H; p.G = (int32_t)s.G;
     p.dt_bf16 = dt->dtype == KDA_BF16; p.softplus = s.softplus;
     p.s0_bf16 = s0 && s0->dtype == KDA_BF16; p.sT_bf16 = sT && sT->dtype == KDA_BF16;
-    p.seg = (int32_t)s.seg; p.slots = (int32_t)s.slots; p.wg_per_slot = (int32_t)s.wps; p.heads_per_wg = s.hpw;
+    p.seg = (int32_t)s.seg; p.own_start = s.own_start; p.slots = (int32_t)s.slots; p.wg_per_slot = (int32_t)s.wps; p.heads_per_wg = s.hpw;
     p.wide = aligned_to(x, 8) && aligned_to(B, 8) && aligned_to(C, 8) && aligned_to(s.tz, 8) && aligned_to(out, 8);
     p.ws_state = (float *)ws;
     p.ws_decay = ws ? (float *)((char *)ws + s.off_decay) : nullptr;
@@ -658,7 +673,7 @@ kda_status_t ssm_run(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_te
     if (s.seg) {
         if ((e = timed("kda_ssm_states", st, [&] { return kda::launch_ssm(p, (int)s.P, (int)s.N, f32, true, st); })) != hipSuccess)
             return hip_fail(e, "segment state launch");
-        if ((e = timed("kda_ssm_scan", st, [&] { return kda::launch_ssm_scan(p, (int)s.P, (int)s.N, st); })) != hipSuccess)
+        if (!p.own_start && (e = timed("kda_ssm_scan", st, [&] { return kda::launch_ssm_scan(p, (int)s.P, (int)s.N, st); })) != hipSuccess)
             return hip_fail(e, "segment scan launch");
     }
     if ((e = timed("kda_ssm", st, [&] { return kda::launch_ssm(p, (int)s.P, (int)s.N, f32, false, st); })) != hipSuccess)

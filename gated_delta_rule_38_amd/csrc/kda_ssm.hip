@@ -232,6 +232,7 @@ struct Place {
     int n;              // sequence
     int64_t tok;        // first token: flat (packed) or within the sequence (dense)
     int len;            // tokens of this workgroup
+    int before, first;  // segments of its sequence before it, and the first one's slot
     bool last;          // the last segment of its sequence
     bool ok;
 };
@@ -289,7 +290,9 @@ __device__ __forceinline__ Place place(const SsmParams &p, int slot)
     const Cut c = cut_of(p, w.n);
     w.last = slot == c.last;
     w.ok = w.last || (slot < room && slot - c.first < c.full);
-    const int64_t from = (int64_t)(w.last ? c.full : slot - c.first) * p.seg;
+    w.first = c.first;
+    w.before = w.last ? c.full : slot - c.first;
+    const int64_t from = (int64_t)w.before * p.seg;
     w.tok = (p.cu ? p.cu[w.n] : 0) + from;
     w.len = w.last ? (int)(c.len - from) : p.seg;
     return w;
@@ -353,9 +356,10 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
     // start state
     f32x4 S[NM];
     float *ws = p.seg ? p.ws_state + ((int64_t)slot * p.H + h) * (N * P) : nullptr;
+    const bool formed = OUT && p.seg && !p.own_start;       // the scan's
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-        if (OUT && p.seg) {
+        if (formed) {
             S[m] = *(const f32x4 *)(ws + ws_index<P, N>(slab, m, lane));
         } else if (OUT && p.s0) {
 #pragma unroll
@@ -364,6 +368,27 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[m][r] = 0.f;
+        }
+    }
+    if (OUT && p.seg && p.own_start && w.before > 0) {
+        // the walk over the segments before this one, the next one's end state in flight
+        const float *end = p.ws_state + ((int64_t)w.first * p.H + h) * (N * P) + ws_index<P, N>(slab, 0, lane);
+        const float *dec = p.ws_decay + (int64_t)w.first * p.H + h;
+        f32x4 e[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) e[m] = *(const f32x4 *)(end + m * 256);
+        for (int k = 0; k < w.before; ++k) {
+            f32x4 next[NM];
+            end += k + 1 < w.before ? (int64_t)p.H * (N * P) : 0;
+#pragma unroll
+            for (int m = 0; m < NM; ++m) next[m] = *(const f32x4 *)(end + m * 256);
+            const float d = dec[(int64_t)k * p.H];
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[m][r] = __builtin_fmaf(S[m][r], d, e[m][r]);
+                e[m] = next[m];
+            }
         }
     }
     auto scale_state = [&](float f) {

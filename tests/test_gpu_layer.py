@@ -471,6 +471,18 @@ def test_ssm_segments_of_packed_batches(kda, lengths, behind):
         assert (out[rows:] == -7.0).all()
 
 
+@pytest.mark.parametrize("P,N,dtype", [(64, 128, "bf16"), (128, 128, "bf16"), (128, 64, "f32")])
+def test_ssm_start_states_both_ways(kda, P, N, dtype):
+    """Final states in place go through the scan's own launch, others mostly not: the same bits."""
+    import torch
+    c = ssm_case([700, 0, 330, 1, 64], 4, 2, P, N, dtype, seed=P + N)
+    for seg in (32, 128, 320):
+        out, fin = kda.ssm_prefill(**c, segment=seg)
+        s0 = c["initial_state"].clone()
+        out2, fin2 = kda.ssm_prefill(**dict(c, initial_state=s0), final_state=s0, segment=seg)
+        assert fin2 is s0 and torch.equal(bits(out), bits(out2)) and torch.equal(fin, s0)
+
+
 def test_layer_without_sequences(kda):
     """cu_seqlens of no sequence: nothing is read or written."""
     import torch
@@ -714,11 +726,13 @@ def test_layer_on_other_stream_and_in_a_graph(kda):
 
 def test_layer_profile_names(kda):
     c = ssm_case([100], 2, 1, 64, 64, "bf16", seed=61)
-    kda.profile_enable(True)
-    try:
-        kda.profile_read()
-        kda.ssm_prefill(**c, segment=32)
-        names = kda.profile_read_kernels()
-    finally:
-        kda.profile_enable(False)
-    assert {k: v[0] for k, v in names.items()} == {"kda_ssm_states": 1, "kda_ssm_scan": 1, "kda_ssm": 1}
+    for final, want in ((None, {"kda_ssm_states": 1, "kda_ssm": 1}),
+                        (c["initial_state"], {"kda_ssm_states": 1, "kda_ssm_scan": 1, "kda_ssm": 1})):
+        kda.profile_enable(True)
+        try:
+            kda.profile_read()
+            kda.ssm_prefill(**c, final_state=final, segment=32)
+            names = kda.profile_read_kernels()
+        finally:
+            kda.profile_enable(False)
+        assert {k: v[0] for k, v in names.items()} == want
