@@ -526,11 +526,12 @@ double ssm_pass(double workgroups, double chunks, double alone, double shared, b
 // outputs' pass reads the end states before its own (16 TB/s, mostly from caches): no launch and no
 // second trip, but bytes that grow with the segments of a sequence (8 prompts, 32,733 tokens, segments
 // of 1,536: 420 us with the scan, 400 without; one of 65,536 in segments of 1,024: 180 and 212).
-// The lengths of a packed batch are on the device: a whole run is charged a longest sequence of 1.7
-// times the mean, whose end it runs alone, and segments half a segment of waste a sequence.
-// On 8 batches of 203 to 65,536 tokens and 4 to 64 heads against 8 forced lengths each the choice is
-// within 10% of the best; on random packed batches up to 28% (where a length happens to fill whole
-// rounds of workgroups, which the host cannot see).
+// The lengths of a packed batch are on the device: the longest is taken for what the longest of n parts
+// of a randomly cut line comes to (ln n + 0.58 times the mean), whose end a whole run is charged for
+// alone, and segments are charged half a segment of waste a sequence.
+// Against 8 to 15 forced lengths each: within 10% of the best on 8 batches of 203 to 65,536 tokens and
+// 4 to 64 heads; on 9 random packed batches 7% over it on average and 24% at most (where a length
+// happens to fill whole rounds of workgroups, which the host cannot see).
 // in_place: the final states replace the initial ones, which other workgroups would still read.
 void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32, bool in_place)
 {
@@ -541,7 +542,7 @@ void ssm_plan(Ssm &s, const kda_ssm_options_t *o, bool f32, bool in_place)
     const int asked = o ? o->segment : 0;
     s.seg = std::max(0, asked);
     const double T = (double)s.L.tokens, n = (double)N, cl = kda::SSM_CHUNK;
-    const double likely = s.L.dense || N == 1 ? (double)longest : std::min((double)longest, 1.7 * T / n);
+    const double likely = s.L.dense || N == 1 ? (double)longest : std::min((double)longest, T / n * (std::log(n) + 0.58));
     // segments of a length, and the cost of their start states
     auto count = [&](int64_t seg) { return s.L.dense || N == 1 ? n * std::ceil((double)longest / (double)seg) : T / (double)seg + 0.5 * n; };
     auto starts = [&](int64_t seg, bool &own) {
