@@ -38,6 +38,19 @@ __device__ __forceinline__ float group_sum(float x, int lanes)
     return x;
 }
 
+// Norm weights at channel c (1 without them), aligned to nothing but their type.
+template <int V>
+__device__ __forceinline__ void weights_at(const float *w, int c, float (&f)[V])
+{
+    typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+        const f32x4_u q = w ? *(const f32x4_u *)(w + c + v) : f32x4_u{1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[v + k] = q[k];
+    }
+}
+
 // V elements as they lie in memory, V sizeof(ET) / 4 words.
 template <typename ET, int V> struct Raw {
     static constexpr int W = V * sizeof(ET) / 4;
@@ -45,7 +58,7 @@ template <typename ET, int V> struct Raw {
     __device__ __forceinline__ void load(const ET *p)
     {
         typedef uint32_t vec __attribute__((ext_vector_type(W)));
-        const vec v = *(const vec *)p;
+        const vec v = __builtin_nontemporal_load((const vec *)p);       // read once: 2% over a plain load
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = v[i];
     }
@@ -64,45 +77,46 @@ template <typename ET, int V> struct Raw {
     }
 };
 
-template <typename ET, int V, int MODE>
+// LANES: of a row; 0: 1 << lanes_log2.
+template <typename ET, int V, int MODE, int LANES>
 __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int lanes_log2)
 {
-    // Rows in flight a lane group.  Packed prefill batch, 40 heads: 2 rows 158 us, 4 rows 172, 8 rows 194
-    // (more registers, fewer waves); one row more requested ahead of each pair 162.
+    // Rows in flight a lane group.
     constexpr int U = 2;
     constexpr bool ROT = MODE != QK_PLAIN;
-    __shared__ float2 sCS[ROT ? 4 : 1][ROT ? 128 : 1];      // a wave's cos and sin
+    __shared__ __attribute__((aligned(16))) float2 sCS[ROT ? 4 : 1][ROT ? 128 : 1];      // a wave's cos and sin
     __shared__ __attribute__((aligned(16))) float sRow[MODE == QK_STRIP ? 4 : 1][MODE == QK_STRIP ? 64 * V : 4];
-    const int wave = threadIdx.x >> 6, lane64 = threadIdx.x & 63;
+    // (what is the same for a wave is kept in scalar registers)
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane64 = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * 4 + wave;
-    const int64_t tok = p.splits == 1 ? item : item / p.splits;
-    const int split = (int)(item - tok * p.splits);
+    const int split = (int)item & (p.splits - 1);           // splits: a power of two
+    const int64_t tok = item >> __builtin_ctz(p.splits);
     if (tok >= p.tokens) return;
-    const int64_t b = p.batched ? tok / p.T : 0, t = tok - b * p.T;
-    const int lanes = 1 << lanes_log2, lane = lane64 & (lanes - 1), slot = lane64 >> lanes_log2, per = 64 >> lanes_log2;
-    const int c0 = lane * V;
-    const bool in = c0 < p.D;
+    const uint32_t b = p.batched ? (uint32_t)tok / (uint32_t)p.T : 0u;
+    const int64_t t = tok - (int64_t)b * p.T;
+    const int lanes = LANES ? LANES : 1 << lanes_log2, per = 64 / lanes;
+    const int lane = lane64 & (lanes - 1), slot = LANES ? lane64 / LANES : lane64 >> lanes_log2;
+    const bool in = lane * V < p.D;
+    const int c0 = in ? lane * V : 0;
 
     Raw<ET, V> x[U];
-    // the rows of one operand: rounds r, r + splits, ... of `per` heads
+    // the rows of one operand: rounds r, r + splits, ... of `per` heads (past the last head: that one
+    // again, not stored)
     const ET *src = nullptr;
     int heads = 0;
     auto load = [&](int s, int r0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = (r0 + u * p.splits) * per + slot;
-            if (h < heads && in) x[u].load(src + h * p.x_sh[s]);
-            else
-#pragma unroll
-                for (int i = 0; i < Raw<ET, V>::W; ++i) x[u].w[i] = 0u;
+            x[u].load(src + min(h, heads - 1) * p.x_sh[s]);
         }
     };
     auto open = [&](int s) {
         src = (const ET *)p.x[s] + b * p.x_sb[s] + t * p.x_st[s] + c0;
         heads = p.heads[s];
+        if (heads > 0) load(s, split);
     };
     open(0);
-    load(0, split);
 
     // this lane's pairs: cos, and sin with the sign its channels take the partner with
     const int half = p.rot >> 1, i0 = c0 - p.offset;
@@ -118,39 +132,55 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int 
             sCS[wave][e] = make_float2(c * p.scale, s * p.scale);
         }
         __builtin_amdgcn_wave_barrier();            // one wave's LDS accesses keep their order
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = i0 + v;
-            const bool rot = i >= 0 && i < p.rot, first = MODE == QK_INTER ? !(i & 1) : i < half;
-            const int e = MODE == QK_INTER ? i >> 1 : (first ? i : i - half);
-            const float2 q = sCS[wave][rot ? e : 0];
-            cs[v] = rot ? q.x : 1.f;
-            sn[v] = rot ? (first ? -q.y : q.y) : 0.f;
-        }
         if constexpr (MODE == QK_LANES) {
             turns = i0 >= 0 && i0 < p.rot;
-            if (turns) partner = lane64 + (i0 < half ? half : -half) / V;
+            const bool first = i0 < half;
+            if (turns) partner = lane64 + (first ? half : -half) / V;
+            const float2 *q = sCS[wave] + (turns ? (first ? i0 : i0 - half) : 0);
+#pragma unroll
+            for (int v = 0; v < V; v += 2) {
+                const float4 two = *(const float4 *)(q + v);
+                cs[v] = turns ? two.x : 1.f;
+                cs[v + 1] = turns ? two.z : 1.f;
+                sn[v] = first ? -two.y : two.y;
+                sn[v + 1] = first ? -two.w : two.w;
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int i = i0 + v;
+                const bool rot = i >= 0 && i < p.rot, first = MODE == QK_INTER ? !(i & 1) : i < half;
+                const int e = MODE == QK_INTER ? i >> 1 : (first ? i : i - half);
+                const float2 q = sCS[wave][rot ? e : 0];
+                cs[v] = rot ? q.x : 1.f;
+                sn[v] = first ? -q.y : q.y;
+            }
         }
     }
+    // what a channel that does not turn takes of its partner is 0, whatever the partner holds
+    auto turning = [&](int v) { return (unsigned)(i0 + v) < (unsigned)p.rot; };
 
     for (int s = 0; s < 2; ++s) {
-        if (s) {
-            open(1);
-            load(1, split);
-        }
+        if (s) open(1);
         if (heads == 0) continue;
         ET *dst = (ET *)p.o[s] + b * p.o_sb[s] + t * p.o_st[s] + c0;
         // out = rn (own A + partner B): the norm weights (own, partner's) and the rotation in one
         float A[V], B[ROT ? V : 1];
+        weights_at<V>(p.w[s], c0, A);
+        if constexpr (MODE == QK_LANES) weights_at<V>(p.w[s], turns ? c0 + (i0 < half ? half : -half) : c0, B);
+        if constexpr (MODE == QK_INTER) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float w = (p.w[s] && in) ? p.w[s][c0 + v] : 1.f;
-            A[v] = ROT ? w * cs[ROT ? v : 0] : w;
-            if constexpr (ROT) {
-                const int i = i0 + v;
-                int far = c0 + v;
-                if (i >= 0 && i < p.rot) far += MODE == QK_INTER ? ((i & 1) ? -1 : 1) : (i < half ? half : -half);
-                B[v] = ((p.w[s] && in) ? p.w[s][far] : 1.f) * sn[v];
+            for (int v = 0; v < V; ++v) B[v] = A[v ^ 1];
+        }
+        if constexpr (MODE == QK_STRIP) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) B[v] = p.w[s] ? p.w[s][c0 + v + (turning(v) ? (i0 + v < half ? half : -half) : 0)] : 1.f;
+        }
+        if constexpr (ROT) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                A[v] *= cs[v];
+                B[v] = turning(v) ? B[v] * sn[v] : 0.f;
             }
         }
         const int rounds = (heads + per - 1) / per;
@@ -167,38 +197,34 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int 
                     float ss = 0.f;
 #pragma unroll
                     for (int v = 0; v < V; ++v) ss = __builtin_fmaf(y[v], y[v], ss);
-                    rn = __builtin_amdgcn_rsqf(__builtin_fmaf(group_sum(ss, lanes), p.inv_d, p.eps));
+                    rn = __builtin_amdgcn_rsqf(__builtin_fmaf(group_sum(in ? ss : 0.f, lanes), p.inv_d, p.eps));
                 }
                 float z[V];
-                if constexpr (MODE == QK_PLAIN) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) z[v] = y[v] * A[v];
-                } else if constexpr (MODE == QK_INTER) {
+                for (int v = 0; v < V; ++v) z[v] = y[v] * A[v];
+                if constexpr (MODE == QK_INTER) {
 #pragma unroll
-                    for (int v = 0; v < V; v += 2) {
-                        // a pair that does not turn takes nothing of each other, not even a NaN
-                        const bool rot = i0 + v >= 0 && i0 + v < p.rot;
-                        z[v] = rot ? __builtin_fmaf(y[v + 1], B[v], y[v] * A[v]) : y[v] * A[v];
-                        z[v + 1] = rot ? __builtin_fmaf(y[v], B[v + 1], y[v + 1] * A[v + 1]) : y[v + 1] * A[v + 1];
-                    }
+                    for (int v = 0; v < V; ++v) z[v] = __builtin_fmaf(turning(v) ? y[v ^ 1] : 0.f, B[v], z[v]);
                 } else if constexpr (MODE == QK_LANES) {
                     Raw<ET, V> far;
                     float other[V];
 #pragma unroll
-                    for (int i = 0; i < Raw<ET, V>::W; ++i) far.w[i] = __builtin_amdgcn_ds_bpermute(partner << 2, x[u].w[i]);
+                    for (int i = 0; i < Raw<ET, V>::W; ++i) {
+                        const uint32_t w = __builtin_amdgcn_ds_bpermute(partner << 2, x[u].w[i]);
+                        far.w[i] = turns ? w : 0u;
+                    }
                     far.unpack(other);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) z[v] = turns ? __builtin_fmaf(other[v], B[v], y[v] * A[v]) : y[v] * A[v];
-                } else {
+                    for (int v = 0; v < V; ++v) z[v] = __builtin_fmaf(other[v], B[v], z[v]);
+                } else if constexpr (MODE == QK_STRIP) {
                     float *strip = sRow[wave] + slot * (lanes * V);
 #pragma unroll
-                    for (int v = 0; v < V; v += 4) *(float4 *)(strip + c0 + v) = make_float4(y[v], y[v + 1], y[v + 2], y[v + 3]);
+                    for (int v = 0; v < V; v += 4) *(float4 *)(strip + lane * V + v) = make_float4(y[v], y[v + 1], y[v + 2], y[v + 3]);
                     __builtin_amdgcn_wave_barrier();
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        const int i = i0 + v;
-                        z[v] = y[v] * A[v];
-                        if (i >= 0 && i < p.rot) z[v] = __builtin_fmaf(strip[c0 + v + (i < half ? half : -half)], B[v], z[v]);
+                        const float other = strip[c0 + v + (turning(v) ? (i0 + v < half ? half : -half) : 0)];
+                        z[v] = __builtin_fmaf(turning(v) ? other : 0.f, B[v], z[v]);
                     }
                     __builtin_amdgcn_wave_barrier();
                 }
@@ -210,19 +236,32 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int 
     }
 }
 
+template <typename ET, int V, int LANES>
+static hipError_t launch_qk_lanes(const QkNormParams &p, bool interleaved, int lg, hipStream_t st)
+{
+    const int64_t blocks = (p.tokens * p.splits + 3) / 4;
+    if (blocks <= 0) return hipSuccess;
+    const dim3 grid((unsigned)blocks), thr(256);
+    if (p.rot == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_PLAIN, LANES>), grid, thr, 0, st, p, lg);
+    else if (interleaved) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_INTER, LANES>), grid, thr, 0, st, p, lg);
+    else if (p.rot / 2 % V == 0 && p.offset % V == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_LANES, LANES>), grid, thr, 0, st, p, lg);
+    else hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_STRIP, LANES>), grid, thr, 0, st, p, lg);
+    return hipGetLastError();
+}
+
+// The usual lane counts (heads of 64 to 256 channels) are known to the compiler: the sum's steps and the
+// rows of a wave need no branches.
 template <typename ET, int V>
 static hipError_t launch_qk_t(const QkNormParams &p, bool interleaved, hipStream_t st)
 {
     int lg = 0;
     while ((V << lg) < p.D) ++lg;
-    const int64_t blocks = (p.tokens * p.splits + 3) / 4;
-    if (blocks <= 0) return hipSuccess;
-    const dim3 grid((unsigned)blocks), thr(256);
-    if (p.rot == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_PLAIN>), grid, thr, 0, st, p, lg);
-    else if (interleaved) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_INTER>), grid, thr, 0, st, p, lg);
-    else if (p.rot / 2 % V == 0 && p.offset % V == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_LANES>), grid, thr, 0, st, p, lg);
-    else hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_STRIP>), grid, thr, 0, st, p, lg);
-    return hipGetLastError();
+    if constexpr (V * sizeof(ET) == 16) {
+        if (lg == 3) return launch_qk_lanes<ET, V, 8>(p, interleaved, lg, st);
+        if (lg == 4) return launch_qk_lanes<ET, V, 16>(p, interleaved, lg, st);
+        if (lg == 5) return launch_qk_lanes<ET, V, 32>(p, interleaved, lg, st);
+    }
+    return launch_qk_lanes<ET, V, 0>(p, interleaved, lg, st);
 }
 
 hipError_t launch_qk_norm(const QkNormParams &p, bool io_f32, int vec, bool interleaved, hipStream_t st)
