@@ -74,7 +74,9 @@ __device__ __forceinline__ void conv_step(float (&win)[W - 1][V], const float (&
 // them write final states (one thread per sequence and channel group), from x and the initial
 // states alone; when the states are updated in place they run as a launch of their own, after
 // every reader.
-template <int W, typename ET, int V>
+// WHOLE: a wave's threads walk one run (cgl >= 6), and its tokens and sequence are kept in scalar
+// registers.
+template <int W, typename ET, int V, bool WHOLE>
 __global__ __launch_bounds__(256) void conv_kernel(const ConvParams p)
 {
     const int cg = threadIdx.x & ((1 << p.cgl) - 1);
@@ -102,7 +104,8 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvParams p)
         return;
     }
     const int cb = blockIdx.x % p.ncb;
-    const int64_t r = (int64_t)(blockIdx.x / p.ncb) * (256 >> p.cgl) + (threadIdx.x >> p.cgl);
+    const int lane_run = threadIdx.x >> p.cgl;
+    const int64_t r = (int64_t)(blockIdx.x / p.ncb) * (256 >> p.cgl) + (WHOLE ? __builtin_amdgcn_readfirstlane(lane_run) : lane_run);
     const int c0 = ((cb << p.cgl) + cg) * V;
     if (c0 >= p.C || r >= p.nrun) return;
     ET *o = (ET *)p.o;
@@ -134,12 +137,13 @@ __global__ __launch_bounds__(256) void conv_kernel(const ConvParams p)
         }
         int m = (int)(stop - f);
         // inputs in flight: packed prefill batch, 12,288 channels: 4 at a time 332 us, 8 at a time 313,
-        // 309 with stores that bypass the caches, 16 at a time 294 (5.5 TB/s; a copy of 2 GB reaches 4.9)
+        // 309 with stores that bypass the caches, 16 at a time 295, 291 with a wave's run in scalar
+        // registers, 286 with loads that bypass them too (runs of 64 tokens: 303, of 128: 309)
         auto steps = [&](auto count) {
             constexpr int K = decltype(count)::value;
             float in[K][V], y[V];
 #pragma unroll
-            for (int u = 0; u < K; ++u) VecIO<ET, V>::load(xp + u * p.x_st, in[u]);
+            for (int u = 0; u < K; ++u) load_once<ET, V>(xp + u * p.x_st, in[u]);
 #pragma unroll
             for (int u = 0; u < K; ++u) {
                 conv_step<W, V>(win, in[u], wt, b, p.silu, y);
@@ -167,8 +171,11 @@ static hipError_t launch_conv_t(const ConvParams &p, int vec, int state_blocks, 
     const int64_t blocks = (int64_t)p.out_blocks + state_blocks;
     if (blocks <= 0) return hipSuccess;
     constexpr int VMAX = sizeof(ET) == 2 ? 8 : 4;
-    if (vec == VMAX) hipLaunchKernelGGL((conv_kernel<W, ET, VMAX>), dim3((unsigned)blocks), dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((conv_kernel<W, ET, 1>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+    const dim3 grid((unsigned)blocks), thr(256);
+    if (vec == VMAX && p.cgl >= 6) hipLaunchKernelGGL((conv_kernel<W, ET, VMAX, true>), grid, thr, 0, st, p);
+    else if (vec == VMAX) hipLaunchKernelGGL((conv_kernel<W, ET, VMAX, false>), grid, thr, 0, st, p);
+    else if (p.cgl >= 6) hipLaunchKernelGGL((conv_kernel<W, ET, 1, true>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((conv_kernel<W, ET, 1, false>), grid, thr, 0, st, p);
     return hipGetLastError();
 }
 

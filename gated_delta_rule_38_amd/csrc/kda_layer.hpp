@@ -46,7 +46,27 @@ template <typename ET, int V> struct VecIO {
     }
 };
 
-// The same store for rows the launch does not read back: non-temporal where a lane writes 16 bytes.
+// The same for rows the launch reads once, or does not read back: non-temporal where a lane moves 16
+// bytes.
+template <typename ET, int V>
+__device__ __forceinline__ void load_once(const ET *p, float (&f)[V])
+{
+    typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+    if constexpr (sizeof(ET) == 2 && V == 8) {
+        const u32v4 w = __builtin_nontemporal_load((const u32v4 *)p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+            f[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+        }
+    } else if constexpr (sizeof(ET) == 4 && V == 4) {
+        const f32x4 w = __builtin_nontemporal_load((const f32x4 *)p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = w[i];
+    } else {
+        VecIO<ET, V>::load(p, f);
+    }
+}
 template <typename ET, int V>
 __device__ __forceinline__ void store_once(ET *p, const float (&f)[V])
 {

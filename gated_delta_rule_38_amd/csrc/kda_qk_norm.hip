@@ -82,7 +82,7 @@ template <typename ET, int V, int MODE, int LANES>
 __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int lanes_log2)
 {
     // Rows in flight a lane group.
-    constexpr int U = 2;
+    constexpr int U = 4;
     constexpr bool ROT = MODE != QK_PLAIN;
     __shared__ __attribute__((aligned(16))) float2 sCS[ROT ? 4 : 1][ROT ? 128 : 1];      // a wave's cos and sin
     __shared__ __attribute__((aligned(16))) float sRow[MODE == QK_STRIP ? 4 : 1][MODE == QK_STRIP ? 64 * V : 4];
