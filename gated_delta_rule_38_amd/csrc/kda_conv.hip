@@ -6,7 +6,10 @@
 // Every input feeds W outputs of its own channel only, so a thread keeps its channels' last W
 // inputs in registers and walks a run of consecutive tokens: each input is read once (W - 1 more
 // at the start of a run), and 64 lanes move 1 KB of consecutive channels at a time.  The bound is
-// HBM: read x, write out; the arithmetic is W FMAs an element.
+// HBM: read x, write out; the arithmetic (W FMAs an element, an exponential and a reciprocal with the
+// activation) is about half of that time.  32,733 tokens x 12,288 channels, width 4, silu, bf16: 284 us,
+// 5.7 TB/s of its 1.61 GB, and 5% more is read at the starts of runs.  256 requests of one token:
+// 9.6 us, 5.3 TB/s.
 #include <type_traits>
 
 #include "kda_layer.hpp"

@@ -12,6 +12,10 @@
 // Rotated pairs sit in one lane (interleaved) or rot / 2 channels apart (half).  When that distance
 // and the offset are whole lanes, the partner's raw channels come by a lane exchange and its norm
 // weight is kept beside the own one; else the row goes through the wave's LDS strip.
+// The arithmetic is near the traffic (about 70 instructions a row and wave), so what is the same for a
+// wave sits in scalar registers and no channel branches: 32,733 tokens, 32 + 8 heads of 128, bf16, half
+// layout: 111 us, 6.1 TB/s of its 0.67 GB (153 us with token and addresses in vector registers and a
+// branch for each channel's partner).
 #include "kda_layer.hpp"
 
 namespace kda {
@@ -77,11 +81,10 @@ template <typename ET, int V> struct Raw {
     }
 };
 
-// LANES: of a row; 0: 1 << lanes_log2.
-template <typename ET, int V, int MODE, int LANES>
+template <typename ET, int V, int MODE>
 __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int lanes_log2)
 {
-    // Rows in flight a lane group.
+    // Rows in flight a lane group (32,733 tokens, 40 heads of 128: 2 rows 116 us, 3 rows 115, 4 rows 113).
     constexpr int U = 4;
     constexpr bool ROT = MODE != QK_PLAIN;
     __shared__ __attribute__((aligned(16))) float2 sCS[ROT ? 4 : 1][ROT ? 128 : 1];      // a wave's cos and sin
@@ -94,8 +97,8 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int 
     if (tok >= p.tokens) return;
     const uint32_t b = p.batched ? (uint32_t)tok / (uint32_t)p.T : 0u;
     const int64_t t = tok - (int64_t)b * p.T;
-    const int lanes = LANES ? LANES : 1 << lanes_log2, per = 64 / lanes;
-    const int lane = lane64 & (lanes - 1), slot = LANES ? lane64 / LANES : lane64 >> lanes_log2;
+    const int lanes = 1 << lanes_log2, per = 64 >> lanes_log2;
+    const int lane = lane64 & (lanes - 1), slot = lane64 >> lanes_log2;
     const bool in = lane * V < p.D;
     const int c0 = in ? lane * V : 0;
 
@@ -236,32 +239,19 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(const QkNormParams p, int 
     }
 }
 
-template <typename ET, int V, int LANES>
-static hipError_t launch_qk_lanes(const QkNormParams &p, bool interleaved, int lg, hipStream_t st)
-{
-    const int64_t blocks = (p.tokens * p.splits + 3) / 4;
-    if (blocks <= 0) return hipSuccess;
-    const dim3 grid((unsigned)blocks), thr(256);
-    if (p.rot == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_PLAIN, LANES>), grid, thr, 0, st, p, lg);
-    else if (interleaved) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_INTER, LANES>), grid, thr, 0, st, p, lg);
-    else if (p.rot / 2 % V == 0 && p.offset % V == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_LANES, LANES>), grid, thr, 0, st, p, lg);
-    else hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_STRIP, LANES>), grid, thr, 0, st, p, lg);
-    return hipGetLastError();
-}
-
-// The usual lane counts (heads of 64 to 256 channels) are known to the compiler: the sum's steps and the
-// rows of a wave need no branches.
 template <typename ET, int V>
 static hipError_t launch_qk_t(const QkNormParams &p, bool interleaved, hipStream_t st)
 {
     int lg = 0;
     while ((V << lg) < p.D) ++lg;
-    if constexpr (V * sizeof(ET) == 16) {
-        if (lg == 3) return launch_qk_lanes<ET, V, 8>(p, interleaved, lg, st);
-        if (lg == 4) return launch_qk_lanes<ET, V, 16>(p, interleaved, lg, st);
-        if (lg == 5) return launch_qk_lanes<ET, V, 32>(p, interleaved, lg, st);
-    }
-    return launch_qk_lanes<ET, V, 0>(p, interleaved, lg, st);
+    const int64_t blocks = (p.tokens * p.splits + 3) / 4;
+    if (blocks <= 0) return hipSuccess;
+    const dim3 grid((unsigned)blocks), thr(256);
+    if (p.rot == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_PLAIN>), grid, thr, 0, st, p, lg);
+    else if (interleaved) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_INTER>), grid, thr, 0, st, p, lg);
+    else if (p.rot / 2 % V == 0 && p.offset % V == 0) hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_LANES>), grid, thr, 0, st, p, lg);
+    else hipLaunchKernelGGL((qk_norm_kernel<ET, V, QK_STRIP>), grid, thr, 0, st, p, lg);
+    return hipGetLastError();
 }
 
 hipError_t launch_qk_norm(const QkNormParams &p, bool io_f32, int vec, bool interleaved, hipStream_t st)

@@ -6,7 +6,8 @@
 // in registers, so each state row moves through HBM once in each direction as whole 16-byte (fp32)
 // or 8-byte (bf16) lanes.  The bound is that traffic.  Decays and updates of a column need no
 // other column, and the read-out's sum over rows is only joined after the last token: two barriers
-// a call, whatever the token count.
+// a call, whatever the token count.  256 requests of one token, 32 heads of 64, 128 state channels, fp32
+// pool: 104 us, 5.2 TB/s of its 0.54 GB.
 #include "kda_layer.hpp"
 
 namespace kda {
@@ -14,7 +15,7 @@ namespace kda {
 typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 
 // State rows are read once and written once by the launch: both bypass the caches (256 requests x 32
-// heads, fp32: 112 us with plain loads, 104 with these, 5.2 TB/s).
+// heads, fp32: 112 us with plain loads, 104 with these).
 __device__ __forceinline__ void ld4_nt(const float *p, float (&x)[4])
 {
     const f32x4 v = __builtin_nontemporal_load((const f32x4 *)p);
