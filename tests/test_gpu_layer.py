@@ -316,6 +316,61 @@ def test_qk_norm_feeds_the_recurrence(kda):
     assert oracle.rel_l2(ref.f64(fin), s_ref) <= 5e-3 + 2 * 2.0 ** -8
 
 
+@pytest.mark.parametrize("layout,rot,offset,D", [("half", 64, 0, 128), ("half", 64, 32, 128), ("half", 36, 4, 96),
+                                                 ("interleaved", 40, 8, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_qk_norm_touches_pairs_alone(kda, layout, rot, offset, D, dtype):
+    """Without a norm a NaN or an infinity reaches itself and, where it turns, its partner; other heads
+    and tokens, and channels that do not turn, never."""
+    import torch
+    q = Draw(D + rot).randn(6, 9, D, dtype=dtype)
+    freq, _ = kda.rotary_frequencies(rot, device="cuda")
+    pos = ints([0, 5, 77, 1000, 3, 8])
+    kw = dict(positions=pos, inv_freq=freq, norm=None, layout=layout, rotary_offset=offset)
+    clean, _ = kda.qk_norm(q, **kw)
+    for c in (0, offset, offset + 1, offset + rot // 2, offset + rot - 1, D - 1):
+        for bad in (float("nan"), float("inf")):
+            x = q.clone()
+            x[2, 4, c] = bad
+            out, _ = kda.qk_norm(x, **kw)
+            hit = {c}
+            if offset <= c < offset + rot:
+                i = c - offset
+                hit.add(offset + (i ^ 1 if layout == "interleaved" else (i + rot // 2) % rot))
+            changed = (bits(out) != bits(clean)).nonzero().tolist()
+            assert {(a, b) for a, b, _ in changed} == {(2, 4)} and {e for _, _, e in changed} <= hit
+            assert not torch.isfinite(out[2, 4, c])
+
+
+def test_qk_norm_weights_at_any_address(kda):
+    """Weights that start between 16-byte boundaries, and q's and k's own."""
+    import torch
+    d = Draw(41)
+    q, k, w = d.randn(9, 4, 128, dtype="bf16"), d.randn(9, 2, 128, dtype="bf16"), d.randn(300)
+    freq, _ = kda.rotary_frequencies(128, device="cuda")
+    kw = dict(positions=ints(range(9)), inv_freq=freq)
+    want = kda.qk_norm(q, k, q_weight=w[1:129].clone(), k_weight=w[131:259].clone(), **kw)
+    got = kda.qk_norm(q, k, q_weight=w[1:129], k_weight=w[131:259], **kw)
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a), bits(b))
+
+
+def test_conv_nan_stays_in_its_sequence_and_channel(kda):
+    """A NaN reaches the W outputs that its input feeds, and the final state where it is one of the last
+    inputs."""
+    import torch
+    c = conv_case([40, 30], 1024, 4, "bf16", "bf16", False, 5)
+    clean, cf = kda.conv(**c, activation="silu")
+    for t, n in ((20, 4), (38, 2)):
+        bad = dict(c, x=c["x"].clone())
+        bad["x"][t, 100] = float("nan")
+        out, fin = kda.conv(**bad, activation="silu")
+        assert torch.isnan(out[t:t + n, 100]).all()
+        changed = (bits(out) != bits(clean)).nonzero().tolist()
+        assert sorted(changed) == [[t + i, 100] for i in range(n)]
+        assert (bits(fin) != bits(cf)).nonzero().tolist() == ([[0, 1, 100]] if t == 38 else [])
+
+
 # ----------------------------------------------------------------------- state space scan
 
 def ssm_case(lengths, H, G, P, N, dtype, seed, gate=True, full=True, dense=False, softplus=True):
@@ -722,6 +777,53 @@ def test_layer_on_other_stream_and_in_a_graph(kda):
             assert torch.equal(bits(a), bits(b)), i
         assert torch.equal(cp, c2) and torch.equal(sp, s2)
     assert given.shape == x.shape
+
+
+def test_layer_device_checks(kda, monkeypatch):
+    """KDA_CHECK=1: bad cu_seqlens and slots named twice are refused before anything runs."""
+    import torch
+    monkeypatch.setenv("KDA_CHECK", "1")
+    d = Draw(91)
+    x, w = d.randn(20, 64, dtype="bf16"), d.randn(64, 4, dtype="bf16")
+    c = ssm_case([20], 2, 1, 64, 64, "bf16", seed=1, full=False)
+    for cu in ([0, 21], [0, 12, 8, 20], [1, 20]):
+        out = torch.full_like(x, -7.0)
+        with pytest.raises(kda.KdaError):
+            kda.conv(x, w, cu_seqlens=ints(cu), out=out)
+        y = torch.full_like(c["x"], -7.0)
+        with pytest.raises(kda.KdaError):
+            kda.ssm_prefill(**dict(c, cu_seqlens=ints(cu)), out=y)
+        assert (out == -7.0).all() and (y == -7.0).all()
+    assert kda.conv(x, w, cu_seqlens=ints([0, 20]))[0].isfinite().all()
+    pool, xs = d.randn(4, 3, 64), d.randn(3, 1, 64, dtype="bf16")
+    states, before = d.randn(4, 2, 64, 64), pool.clone()
+    s = {k: v for k, v in ssm_case([1] * 3, 2, 1, 64, 64, "bf16", seed=2, dense=True, full=False).items()
+         if k not in ("cu_seqlens", "initial_state")}
+    with pytest.raises(kda.KdaError):
+        kda.conv_decode(xs, w, pool, ints([2, 1, 2]))
+    with pytest.raises(kda.KdaError):
+        kda.ssm_decode(**s, state_pool=states, state_indices=ints([2, 1, 2]))
+    assert torch.equal(pool, before)
+    # reading one slot twice is allowed, and gives equal requests equal outputs
+    xs[2] = xs[0]
+    out = kda.conv_decode(xs, w, pool, ints([2, 1, 2]), update_state=False)
+    assert torch.equal(bits(out[0]), bits(out[2])) and torch.equal(pool, before)
+    kda.conv_decode(xs, w, pool, ints([2, 1, -1]))
+
+
+def test_ssm_workspace_misuse(kda):
+    import torch
+    c = ssm_case([300], 2, 1, 64, 64, "bf16", seed=7)
+    need = kda.ssm_workspace_size(*(c[k] for k in ("x", "dt", "A", "B", "C", "initial_state", "cu_seqlens")), segment=64)
+    want, wf = kda.ssm_prefill(**c, segment=64)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")       # NaN in every word
+    out, fin = kda.ssm_prefill(**c, segment=64, workspace=ws)
+    assert torch.equal(bits(out), bits(want)) and torch.equal(fin, wf)
+    with pytest.raises(kda.KdaError):
+        kda.ssm_prefill(**c, segment=64, workspace=ws[:need // 2])
+    for bad in (torch.empty(need + 256, dtype=torch.uint8), ws[::2], 5):
+        with pytest.raises(ValueError):
+            kda.ssm_prefill(**c, segment=64, workspace=bad)
 
 
 def test_layer_profile_names(kda):
