@@ -175,6 +175,7 @@ struct SsmParams {
     int32_t dt_bf16, softplus, s0_bf16, sT_bf16;
     int32_t seg;               // tokens per segment (a multiple of SSM_CHUNK); 0: whole sequences
     int32_t slots;             // segment slots (seg > 0) or sequences: the last N for last segments
+    int32_t fine;              // 16 bits in what only feeds the output (bf16 data)
     int32_t own_start;         // workgroups form their own start states (else the scan did)
     int32_t wg_per_slot;       // workgroups of one slot
     int32_t heads_per_wg;

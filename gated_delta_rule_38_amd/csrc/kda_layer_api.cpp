@@ -507,6 +507,10 @@ kda_status_t ssm_state(const kda_tensor_t *t, const char *name, int64_t n, int64
     return KDA_OK;
 }
 
+// Up to this many workgroups every one has a CU to itself, and keeps 16 bits in what only feeds the
+// output (FINE in kda_ssm.hip).
+constexpr int64_t SSM_CUS = 256;
+
 // Microseconds of one pass over `chunks` chunks by `workgroups` workgroups: `alone` a chunk while every
 // workgroup has its CU to itself, towards `shared` as two sit on some CUs (the pass ends with those)
 // and on all (512 at once), rounds beyond that; one is the most a CU holds of the fp32 kernel.
@@ -665,7 +669,8 @@ kda_status_t ssm_run(const kda_tensor_t *x, const kda_tensor_t *dt, const kda_te
     p.N = (int32_t)s.L.N; p.T = (int32_t)s.L.T; p.H = (int32_t)s.H; p.G = (int32_t)s.G;
     p.dt_bf16 = dt->dtype == KDA_BF16; p.softplus = s.softplus;
     p.s0_bf16 = s0 && s0->dtype == KDA_BF16; p.sT_bf16 = sT && sT->dtype == KDA_BF16;
-    p.seg = (int32_t)s.seg; p.own_start = s.own_start; p.slots = (int32_t)s.slots; p.wg_per_slot = (int32_t)s.wps; p.heads_per_wg = s.hpw;
+    p.seg = (int32_t)s.seg; p.own_start = s.own_start;
+    p.fine = s.slots * s.wps <= SSM_CUS; p.slots = (int32_t)s.slots; p.wg_per_slot = (int32_t)s.wps; p.heads_per_wg = s.hpw;
     p.wide = aligned_to(x, 8) && aligned_to(B, 8) && aligned_to(C, 8) && aligned_to(s.tz, 8) && aligned_to(out, 8);
     p.ws_state = (float *)ws;
     p.ws_decay = ws ? (float *)((char *)ws + s.off_decay) : nullptr;

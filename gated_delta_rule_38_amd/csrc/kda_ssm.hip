@@ -28,7 +28,8 @@
 //
 // Precision on bf16 data: x, B, C enter exactly; weighted x is split into three bf16 parts (24
 // bits) for the state update, so states carry fp32 precision, and two of them (16 bits) feed the
-// output; B C^T and the copy of the state that only feed the bf16 output are rounded to bf16 once.
+// output; B C^T and the copy of the state that only feed the bf16 output are rounded to bf16 once, or
+// where workgroups are few kept in two parts.
 //
 // Sequences too few to fill the chip are cut into segments of equal length: pass 1 runs every
 // segment but the last of its sequence from a zero state (state update only), the end states are
@@ -172,6 +173,22 @@ __device__ __forceinline__ void split3(const float (&f)[8], Frag8<bf16> (&o)[3])
     }
 }
 
+// What rounding 8 fp32 values to bf16 leaves of them, rounded to bf16.
+__device__ __forceinline__ void rest_of(const float (&f)[8], Frag8<bf16> &o)
+{
+    Frag8<bf16> hi;
+    hi.set(f);
+    const uint4 u = __builtin_bit_cast(uint4, hi.v);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        r[2 * e] = f[2 * e] - __builtin_bit_cast(float, w[e] << 16);
+        r[2 * e + 1] = f[2 * e + 1] - __builtin_bit_cast(float, w[e] & 0xffff0000u);
+    }
+    o.set(r);
+}
+
 // 2^x of a 64-bit exponent, to 32-bit precision: the whole part goes into the exponent bits.
 __device__ __forceinline__ float exp2_of(double x)
 {
@@ -313,9 +330,14 @@ __device__ __forceinline__ int ws_index(int slab, int m, int lane) { return ((sl
 // Channel of register r of tile m (lane group g = lane / 16).
 __device__ __forceinline__ int row_of(int m, int g, int r) { return 32 * (m >> 1) + 8 * g + 4 * (m & 1) + r; }
 
-// GATED: z is given.
-template <typename ET, int P, int N, int HPW, bool OUT, bool GATED>
-__global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kernel(const SsmParams p)
+// GATED: z is given.  FINE (bf16, as many workgroups as CUs or fewer): what only feeds the output, B C^T
+// and the state's copy, keeps 16 bits too, so that the output's own rounding is all that is left of it.
+// In few outputs the roundings are not evened out (on 10 tokens an error of 2.2e-3 was met where the
+// output's rounding alone makes 1.3e-3), and with one workgroup on a CU it costs nothing: 10 to 2,048
+// tokens in up to 256 workgroups take the same time within 2%.  Its registers let one workgroup into a
+// CU instead of two: 16 x 2,048 tokens of 64 heads take 405 us with it and 286 without.
+template <typename ET, int P, int N, int HPW, bool OUT, bool GATED, bool FINE>
+__global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? (FINE ? 2 : 4) : 1) void ssm_kernel(const SsmParams p)
 {
     constexpr int NW = HPW * P / 16, NT = NW * 64;      // waves, threads
     constexpr int SLABS = P / 16, NM = N / 16, NA = N / 32, XC = HPW * P;
@@ -327,6 +349,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
     __shared__ __attribute__((aligned(16))) ET sX[2][L * XC];
     __shared__ __attribute__((aligned(16))) ET sZ[GATED ? 2 : 1][GATED ? L * XC : 4];
     __shared__ __attribute__((aligned(16))) ET sM[OUT ? L * L : 4];     // C B^T, j <= i: row i, units of 4 j
+    __shared__ __attribute__((aligned(16))) ET sRest[FINE ? L * L : 4];  // what sM's rounding left
     // of a group's chunks and heads, for each token: step, sum of a, weight of x, decay of y
     __shared__ __attribute__((aligned(16))) float sStep[2][GC][HPW][L], sWt[2][GC][HPW][L], sEi[OUT ? 2 : 1][GC][HPW][L];
     __shared__ __attribute__((aligned(16))) float2 sSum[2][GC][HPW][L];
@@ -500,6 +523,7 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
         if constexpr (OUT) {
             if (tid < L * L / 8) *(f32x4 *)((char *)sM + tid * 8 * sizeof(ET)) = f32x4{0.f, 0.f, 0.f, 0.f};
             if (sizeof(ET) == 4 && tid < L * L / 8) *(f32x4 *)((char *)sM + tid * 32 + 16) = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (FINE && tid < L * L / 8) *(f32x4 *)((char *)sRest + tid * 16) = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         const float dt0 = load_dt(0);
         dt_next = load_dt(1);
@@ -552,6 +576,13 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
 #pragma unroll
                 for (int r = 0; r < 4; ++r) m4[r] = (jt != it || 4 * g + r <= l16) ? G[r] : 0.f;
                 Vec4<ET>::store(sM + m_at(16 * it + l16, 4 * jt + g), Vec4<ET>::pack(m4));
+                if constexpr (FINE) {
+                    float hi[4];
+                    Vec4<ET>::unpack(Vec4<ET>::pack(m4), hi);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) m4[r] -= hi[r];
+                    Vec4<ET>::store(sRest + m_at(16 * it + l16, 4 * jt + g), Vec4<ET>::pack(m4));
+                }
             }
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
@@ -563,6 +594,14 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                 for (int it = 0; it < 2; ++it) {
                     fc.load8(tC + rn.at(it, a));
                     mma16(Y[it], fs, fc);           // (Z^T C^T)[p][i]
+                }
+                if constexpr (FINE) {
+                    rest_of(t8, fs);
+#pragma unroll
+                    for (int it = 0; it < 2; ++it) {
+                        fc.load8(tC + rn.at(it, a));
+                        mma16(Y[it], fs, fc);
+                    }
                 }
             }
         }
@@ -610,6 +649,13 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                 for (int i = 0; i < (BF ? 2 : 1); ++i)
 #pragma unroll
                     for (int it = 0; it < 2; ++it) mma16(Y[it], fw[i], fm[it]);
+                if constexpr (FINE) {
+#pragma unroll
+                    for (int it = 0; it < 2; ++it) {
+                        fm[it].load44(sRest + m_at(16 * it + l16, g), sRest + m_at(16 * it + l16, 4 + g));
+                        mma16(Y[it], fw[0], fm[it]);
+                    }
+                }
             } else {
                 // every weight a difference of sums: step_j e^{c_i - c_j} on M, plain x.  (The
                 // addresses are formed here: held through the loop they would cost its registers.)
@@ -629,6 +675,16 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                             m8[2 * e] = __builtin_bit_cast(float, vw[e] << 16);
                             m8[2 * e + 1] = __builtin_bit_cast(float, vw[e] & 0xffff0000u);
                         }
+                        if constexpr (FINE) {
+                            fd.load44(sRest + m_at(16 * it + hi, hg), sRest + m_at(16 * it + hi, 4 + hg));
+                            const uint4 q = __builtin_bit_cast(uint4, fd.v);
+                            const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                m8[2 * e] += __builtin_bit_cast(float, qw[e] << 16);
+                                m8[2 * e + 1] += __builtin_bit_cast(float, qw[e] & 0xffff0000u);
+                            }
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) m8[e] = fd.v[e];
@@ -647,6 +703,10 @@ __global__ __launch_bounds__(HPW * P * 4, sizeof(ET) == 2 ? 4 : 1) void ssm_kern
                     for (int r = 0; r < 4; ++r) Y[it][r] *= ei[it];
                     Cols<ET, XC, false>(hl, wh * P + slab * 16).get(fp, tX, 0, 0);
                     mma16(Y[it], fp, fd);
+                    if constexpr (FINE) {
+                        rest_of(m8, fd);
+                        mma16(Y[it], fp, fd);
+                    }
                     ei[it] = 1.f;
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -744,9 +804,12 @@ static hipError_t launch_t(const SsmParams &p, bool states_only, hipStream_t st)
     const int64_t blocks = (int64_t)(states_only ? p.slots - p.N : p.slots) * p.wg_per_slot;
     if (blocks <= 0) return hipSuccess;
     const dim3 grid((unsigned)blocks), thr(HPW * P * 4);
-    if (states_only) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, false, false>), grid, thr, 0, st, p);
-    else if (p.z) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, true>), grid, thr, 0, st, p);
-    else hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, false>), grid, thr, 0, st, p);
+    constexpr bool BF = sizeof(ET) == 2;
+    if (states_only) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, false, false, false>), grid, thr, 0, st, p);
+    else if (BF && p.fine && p.z) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, true, BF>), grid, thr, 0, st, p);
+    else if (BF && p.fine) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, false, BF>), grid, thr, 0, st, p);
+    else if (p.z) hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, true, false>), grid, thr, 0, st, p);
+    else hipLaunchKernelGGL((ssm_kernel<ET, P, N, HPW, true, false, false>), grid, thr, 0, st, p);
     return hipGetLastError();
 }
 

@@ -110,7 +110,7 @@ typedef struct {
  * A step > 0, follows the same formula while a chunk grows by less than 2^96).
  * Chunks of 32 tokens run on the matrix cores.  On bf16 data products of inputs are exact, the
  * state's additive term keeps 24 bits, and the state and the products of B and C are rounded to bf16
- * where they only feed out.  Terms are weighted by up to 2^96 against each other, so |x B C| (and
+ * where they only feed out (to 16 bits where no two workgroups share a CU).  Terms are weighted by up to 2^96 against each other, so |x B C| (and
  * their sums) may reach 2^31.  A NaN or infinity in x or dt at a token can reach the outputs of up to
  * 31 tokens before it in its sequence, never another sequence, and only its own head.
  * Rows behind cu[N] are not read and left as they were.  Token strides below 2^24 - 256 elements and

@@ -506,6 +506,24 @@ def test_ssm_empty_and_behind(kda):
     assert torch.equal(none[1], c["initial_state"])
 
 
+@pytest.mark.parametrize("lengths", [[1], [10], [1, 2, 0, 30], [33, 0, 170]])
+@pytest.mark.parametrize("H,G,P,N", [(2, 1, 64, 128), (1, 1, 64, 64), (2, 2, 128, 64), (2, 1, 128, 128)])
+@pytest.mark.parametrize("gate", [True, False])
+def test_ssm_few_tokens_round_once(kda, lengths, H, G, P, N, gate):
+    """bf16 batches of few tokens: two bf16 parts (a rest of 2^-16) of the weighted x, of B C^T and of the
+    state that feeds the output, so 3 x 2^-16 of the magnitudes beside the output's one rounding.  Some
+    heads decay by more than 2^96 a chunk."""
+    c = ssm_case(lengths, H, G, P, N, "bf16", seed=sum(lengths) + P + N, gate=gate)
+    for strong in (False, True):
+        if strong:
+            c["A"][0] = -60.0
+        out, fin = kda.ssm_prefill(**c)
+        w, f, mag, fmag = ssm_ref(c)
+        acc = (512 + max(lengths)) * 2.0 ** -24
+        within(out, w, (acc + 3 * 2.0 ** -16) * mag + U["bf16"] * np.abs(w), "out")
+        within(fin, f, acc * fmag, "final state")
+
+
 @pytest.mark.parametrize("lengths", [[64, 64, 0, 128, 65, 63, 1], [192, 96, 96], [0, 0, 31, 0], [97, 1, 1, 1, 127]])
 @pytest.mark.parametrize("behind", [0, 70])
 def test_ssm_segments_of_packed_batches(kda, lengths, behind):
